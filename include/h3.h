@@ -526,6 +526,89 @@ int h3_qkv_qknorm_mrope_sp_e4m3(const h3_dims* dims, const h3_ranges* shard, con
 int h3_attention_sp(const h3_dims* dims, const h3_sp_layout* layout, const h3_sp_peers* peers,
                     const h3_bf16* qn_w, const h3_bf16* kn_w, int flags, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Backward pass of the block: the gradient of each of its calls, for
+ * fine-tuning the trunk.  Every call takes what its forward call took and the
+ * gradient of what it wrote, and recomputes the rest (statistics, q and k
+ * before their norm, gate and up, the probabilities), so a training step keeps
+ * per block only x before each branch, q, k, v, o and lse.
+ *   - The gradient of the residual stream is fp32 [L_pad][D], of bf16
+ *     activations bf16, and of weights, norm weights and modulation bf16 (sums
+ *     in fp32, rounded once).  dmod [3][6][D] bf16: each call writes its own
+ *     slots for all three modalities (0 where a modality has no tokens) and
+ *     leaves the others.
+ *   - Outputs are overwritten, not accumulated.  Gradients of weights, norm
+ *     weights and modulation may be NULL: not computed (frozen weights).
+ *   - Padding rows (>= L) of the backward calls' inputs are not read, whatever
+ *     they hold; of outputs over tokens they are written as 0.
+ *   - Outputs and ws must not overlap each other or any input, except that dx
+ *     of h3_adaln_norm_modulate_backward may be dres.
+ *   - Sums run in a fixed order: the same call gives the same bits.
+ *   - ws: caller-owned scratch of h3_backward_workspace_bytes() bytes for the
+ *     operation, 16-byte aligned; nothing in it outlives the call's kernels. */
+enum h3_backward_op {
+  H3_BWD_ADALN = 0,
+  H3_BWD_QKV = 1,
+  H3_BWD_ATTENTION = 2,
+  H3_BWD_GATED_RESIDUAL = 3,
+  H3_BWD_FFN = 4
+};
+
+/* Host only.  Workspace bytes of one backward call at L_pad rows (0 for
+ * invalid arguments). */
+size_t h3_backward_workspace_bytes(const h3_dims* dims, int L_pad, int op);
+
+/* Backward of h3_adaln_norm_modulate (same x, mod, branch), joined with the
+ * residual branch around it: with dxm the gradient of xm and dres the gradient
+ * that reaches x past the branch,
+ *   dx = dres + LayerNorm'(x)^T (dxm (1 + scale_m)),
+ * dmod slots shift, scale of the branch: sums over each modality's rows of dxm
+ * and of dxm LayerNorm(x).
+ *   x [L_pad][D] fp32; dxm [L_pad][D] bf16; dres, dx [L_pad][D] fp32. */
+int h3_adaln_norm_modulate_backward(const h3_dims* dims, const h3_ranges* ranges, const float* x, const float* mod,
+                                    int branch, const h3_bf16* dxm, const float* dres, float* dx, h3_bf16* dmod,
+                                    void* ws, void* stream);
+
+/* Backward of h3_qkv_qknorm_mrope with H3_QK_NORM_ROPE_IN_QKV: from dq, dk, dv
+ * [H][L_pad][128] (gradients of the normalised and rotated q, k, and of v),
+ *   dxm [L_pad][D], dWqkv [3I][D], dqn_w, dkn_w [128], all bf16.
+ * q and k before their norm are taken again from xm and Wqkv. */
+int h3_qkv_qknorm_mrope_backward(const h3_dims* dims, const h3_ranges* ranges, const h3_bf16* xm,
+                                 const h3_bf16* Wqkv, const h3_bf16* qn_w, const h3_bf16* kn_w, const float* pos,
+                                 const h3_bf16* dq, const h3_bf16* dk, const h3_bf16* dv, h3_bf16* dxm,
+                                 h3_bf16* dWqkv, h3_bf16* dqn_w, h3_bf16* dkn_w, void* ws, void* stream);
+
+/* h3_attention with H3_QK_NORM_ROPE_IN_QKV on bf16 q, k, which also keeps each
+ * row's log-sum-exp for the backward pass:
+ *   lse [H][L_pad] fp32, lse_i = log(sum_j exp(q_i k_j / sqrt(128))) over the L
+ *   valid keys; 0 in padding rows.
+ * o is the same as h3_attention's, bit for bit. */
+int h3_attention_lse(const h3_dims* dims, const h3_ranges* ranges, const h3_bf16* q, const h3_bf16* k,
+                     const h3_bf16* v, const h3_bf16* qn_w, const h3_bf16* kn_w, h3_bf16* o, float* lse,
+                     void* stream);
+
+/* Backward of h3_attention_lse (same q, k, v; its o and lse): from d_o, the
+ * gradient of o [L_pad][H*128], the gradients dq, dk, dv [H][L_pad][128] bf16.
+ * The probabilities are recomputed from lse. */
+int h3_attention_backward(const h3_dims* dims, const h3_ranges* ranges, const h3_bf16* q, const h3_bf16* k,
+                          const h3_bf16* v, const h3_bf16* o, const float* lse, const h3_bf16* d_o, h3_bf16* dq,
+                          h3_bf16* dk, h3_bf16* dv, void* ws, void* stream);
+
+/* Backward of h3_gated_residual (same o, Wo, mod, branch): from dx, the gradient
+ * of the updated x (which is also the gradient of the x it was added to),
+ *   d_o [L_pad][I] bf16 = (gate_m (.) dx) Wo,  dWo [D][I] bf16,
+ *   dmod slot gate of the branch. */
+int h3_gated_residual_backward(const h3_dims* dims, const h3_ranges* ranges, const float* dx, const h3_bf16* o,
+                               const h3_bf16* Wo, const float* mod, int branch, h3_bf16* d_o, h3_bf16* dWo,
+                               h3_bf16* dmod, void* ws, void* stream);
+
+/* Backward of h3_ffn_swiglu (same xm, Wgu, Wd, mod): from dx, the gradient of
+ * the updated x, dxm [L_pad][D], dWgu [2F][D], dWd [D][F] bf16 and dmod slot
+ * gate_mlp.  Gate and up are taken again from xm. */
+int h3_ffn_swiglu_backward(const h3_dims* dims, const h3_ranges* ranges, const float* dx, const h3_bf16* xm,
+                           const h3_bf16* Wgu, const h3_bf16* Wd, const float* mod, h3_bf16* dxm, h3_bf16* dWgu,
+                           h3_bf16* dWd, h3_bf16* dmod, void* ws, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

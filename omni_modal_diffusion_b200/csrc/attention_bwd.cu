@@ -1,0 +1,574 @@
+// Backward pass of the non-causal attention of the packed sequence on tcgen05
+// tensor cores.  With S = Q K^T, c = 1 / sqrt(128), P = exp(c S - lse) row by
+// row (lse: the forward call's log-sum-exp) and delta = rowsum(dO (.) O):
+//   dV = P^T dO,  dP = dO V^T,  dS = P (.) (dP - delta),
+//   dQ = c dS K,  dK = c dS^T Q.
+// The probabilities are recomputed, never stored.
+//
+// Two kernels instead of one: attention_bwd_kv_kernel owns a key tile and walks
+// the queries (dK, dV), attention_bwd_q_kernel owns a query tile and walks the
+// keys (dQ).  S and dP are taken twice, seven tile products instead of five,
+// but each result then lives in one CTA's TMEM: no fp32 dQ in memory, no
+// atomics (the same call gives the same bits), and P^T and dS go from the
+// registers that computed them to TMEM as the next product's A operand.  One
+// kernel with five products has to turn dS through shared memory and add a
+// 64 KB dQ tile per step to memory: 256 KB of MMA operands, 32 KB of dS and
+// 128 KB of dQ through the 128 B/clk of shared memory are 3,300 clocks a tile
+// pair, against 3,584 clocks of tensor time for the seven.
+//
+// P and dS are rounded to bf16 for their products (relative 2^-9 each, as the
+// forward pass rounds P); sums, exponentials and the subtraction are fp32.
+//
+// Valid rows end inside a tile: the tensor maps stop at token L, TMA reads
+// zeros past it (whatever the padding rows hold), masked queries have
+// lse = +inf (P = 0), and masked keys are set to P = 0 in the last key tile.
+#include "h3_internal.cuh"
+#include "ptx.cuh"
+
+namespace h3 {
+
+namespace attn_bwd {
+using attn_detail::HALF_BYTES;
+using attn_detail::TILE;
+using attn_detail::TILE_BYTES;
+using attn_split::tmem_st16;
+
+// Warp 0 TMA, warp 1 MMA, warps 2-17 elementwise: lane quarter w % 4, 32 of the
+// tile's 128 columns
+constexpr int THREADS = 18 * 32;
+constexpr int CWARPS = 16;
+
+// ------------------------------------------------------------ row statistics
+// nlse2[h][r] = -lse log2(e) (-inf past L: P = 0), ndelta[h][r] = -sum_d do o
+// (0 past L).  16 threads per (row, head), 8 elements each.
+__global__ void __launch_bounds__(256) attention_delta_kernel(const bf16* __restrict__ o, const bf16* __restrict__ d,
+                                                              const float* __restrict__ lse, int H, int L, int L_pad,
+                                                              float* __restrict__ nlse2, float* __restrict__ ndelta) {
+  const long total = (long)L_pad * H * 16;
+  for (long i = blockIdx.x * 256L + threadIdx.x; i < total; i += gridDim.x * 256L) {
+    const long rh = i >> 4;
+    const int row = (int)(rh / H), h = (int)(rh - (long)row * H);
+    float s = 0.f;
+    if (row < L) {
+      const uint4 a = __ldcs(reinterpret_cast<const uint4*>(o) + i), b = __ldcs(reinterpret_cast<const uint4*>(d) + i);
+      const __nv_bfloat162 *pa = reinterpret_cast<const __nv_bfloat162*>(&a),
+                           *pb = reinterpret_cast<const __nv_bfloat162*>(&b);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = __bfloat1622float2(pa[j]), y = __bfloat1622float2(pb[j]);
+        s = fmaf(x.x, y.x, s);
+        s = fmaf(x.y, y.y, s);
+      }
+    }
+#pragma unroll
+    for (int k = 8; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    if ((threadIdx.x & 15) == 0) {
+      const long at = (long)h * L_pad + row;
+      ndelta[at] = -s;
+      nlse2[at] = row < L ? -lse[at] * 1.4426950408889634f : -INFINITY;
+    }
+  }
+}
+
+struct BwdMaps {
+  CUtensorMap q, k, v;  // [H][L][128] (row stride 128, head stride L_pad * 128)
+  CUtensorMap d;        // dO, token-major [L][H * 128]
+};
+
+__device__ __forceinline__ void load_head_tile(uint8_t* dst, const CUtensorMap* m, uint64_t* bar, int row, int h) {
+  tma_load_3d(dst, m, bar, 0, row, h);
+  tma_load_3d(dst + HALF_BYTES, m, bar, 64, row, h);
+}
+__device__ __forceinline__ void load_token_tile(uint8_t* dst, const CUtensorMap* m, uint64_t* bar, int row, int h) {
+  tma_load_2d(dst, m, bar, h * 128, row);
+  tma_load_2d(dst + HALF_BYTES, m, bar, h * 128 + 64, row);
+}
+
+// D = A B^T over d = 128, both K-major 128 x 128 tiles
+__device__ __forceinline__ void mma_abt(uint32_t d_tmem, uint64_t ad, uint64_t bd) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) {
+    const uint64_t off = (uint64_t)(((kk >> 2) * HALF_BYTES + (kk & 3) * 32) >> 4);
+    umma_bf16(d_tmem, ad + off, bd + off, idesc, kk != 0 ? 1u : 0u);
+  }
+}
+// D (+)= A B over 128 rows of B: A packed bf16 in TMEM, columns of 32-wide group
+// g at a_tmem + 32 g .. + 16; B a 128 x 128 tile taken MN-major
+__device__ __forceinline__ void mma_tmem_ab(uint32_t d_tmem, uint32_t a_tmem, uint64_t bd, bool accumulate) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, true);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    umma_bf16_tmem_a(d_tmem, a_tmem + (kk >> 1) * 32 + (kk & 1) * 8, bd + (uint64_t)((kk * 2048) >> 4), idesc,
+                     (accumulate || kk != 0) ? 1u : 0u);
+}
+
+// 32 columns of one row of an fp32 accumulator, scaled, as bf16
+__device__ __forceinline__ void store_cols32(uint32_t taddr, float scale, bf16* dst) {
+  float v[32];
+  tmem_ld32(taddr, reinterpret_cast<uint32_t*>(v));
+  tmem_wait_ld();
+#pragma unroll
+  for (int j = 0; j < 32; j += 8)
+    *reinterpret_cast<uint4*>(dst + j) =
+        make_uint4(pack_bf16x2(v[j] * scale, v[j + 1] * scale), pack_bf16x2(v[j + 2] * scale, v[j + 3] * scale),
+                   pack_bf16x2(v[j + 4] * scale, v[j + 5] * scale), pack_bf16x2(v[j + 6] * scale, v[j + 7] * scale));
+}
+__device__ __forceinline__ void zero_cols32(bf16* dst) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 8) *reinterpret_cast<uint4*>(dst + j) = make_uint4(0, 0, 0, 0);
+}
+
+// ------------------------------------------------------------ dK, dV
+// TMEM: S^T [0, 128) (P^T over it), dP^T [128, 256) (dS^T over it), dV, dK.
+// Tensor and elementwise work alternate between the two score tiles:
+//   exponentials of S^T(i)      while the tensor core runs dK(i - 1), dP^T(i)
+//   dS^T(i) from dP^T(i)        while it runs dV(i), S^T(i + 1)
+struct KvLayout {
+  static constexpr int K = 0, V = TILE_BYTES, Q = 2 * TILE_BYTES, D = 4 * TILE_BYTES;  // Q, dO: two stages
+  static constexpr int STAT = 6 * TILE_BYTES;  // [2][-lse log2 e, -delta][128]
+  static constexpr int BAR = STAT + 2 * 2 * 128 * 4;
+  static constexpr int BYTES = BAR + 256 + 1024;
+  static_assert(BYTES <= 232448, "shared memory per CTA");
+};
+
+__global__ void __launch_bounds__(THREADS, 1)
+    attention_bwd_kv_kernel(const __grid_constant__ BwdMaps maps, const float* __restrict__ nlse2,
+                            const float* __restrict__ ndelta, int L, int L_pad, float scale, float scale_log2,
+                            bf16* __restrict__ dk, bf16* __restrict__ dv) {
+  using Y = KvLayout;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Y::BAR);
+  uint64_t* kv_full = bars + 0;
+  uint64_t* q_full = bars + 1;    // [2] Q and its rows' statistics
+  uint64_t* q_empty = bars + 3;   // [2] after dK of the tile
+  uint64_t* d_full = bars + 5;    // [2]
+  uint64_t* d_empty = bars + 7;   // [2] after dV of the tile
+  uint64_t* s_full = bars + 9;
+  uint64_t* dp_full = bars + 10;
+  uint64_t* p_ready = bars + 11;
+  uint64_t* ds_ready = bars + 12;
+  uint64_t* acc_full = bars + 13;
+  uint64_t* drain = bars + 14;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int key0 = blockIdx.x * TILE, h = blockIdx.y;
+  const int n_q = (L + TILE - 1) / TILE;
+  if (key0 >= L) {  // a tile of padding rows
+    for (int i = threadIdx.x; i < TILE * 16; i += THREADS) {
+      const long at = ((long)h * L_pad + key0 + (i >> 4)) * 16 + (i & 15);
+      reinterpret_cast<uint4*>(dk)[at] = make_uint4(0, 0, 0, 0);
+      reinterpret_cast<uint4*>(dv)[at] = make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], 1);
+      mbar_init(&d_full[s], 1);
+      mbar_init(&d_empty[s], 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(p_ready, CWARPS);
+    mbar_init(ds_ready, CWARPS);
+    mbar_init(acc_full, 1);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&maps.q);
+    tma_prefetch_desc(&maps.d);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(kv_full, 2 * TILE_BYTES);
+      load_head_tile(smem + Y::K, &maps.k, kv_full, key0, h);
+      load_head_tile(smem + Y::V, &maps.v, kv_full, key0, h);
+      long long q_issued = 0, d_issued = 0;
+      for (int i = 0; i < n_q; ++i) {
+        const int st = i & 1;
+        const uint32_t ph = ((i >> 1) & 1) ^ 1;
+        if (!mbar_wait(&q_empty[st], ph)) break;
+        mbar_arrive_expect_tx(&q_full[st], TILE_BYTES + 2 * 128 * 4);
+        load_head_tile(smem + Y::Q + st * TILE_BYTES, &maps.q, &q_full[st], i * TILE, h);
+        const long at = (long)h * L_pad + i * TILE;
+        bulk_load(smem + Y::STAT + st * 1024, nlse2 + at, 512, &q_full[st]);
+        bulk_load(smem + Y::STAT + st * 1024 + 512, ndelta + at, 512, &q_full[st]);
+        ++q_issued;
+        if (!mbar_wait(&d_empty[st], ph)) break;
+        mbar_arrive_expect_tx(&d_full[st], TILE_BYTES);
+        load_token_tile(smem + Y::D + st * TILE_BYTES, &maps.d, &d_full[st], i * TILE, h);
+        ++d_issued;
+      }
+      mbar_wait(kv_full, 0);
+      drain_loads(q_full, 2, q_issued);
+      drain_loads(d_full, 2, d_issued);
+    }
+  } else if (warp == 1) {
+    const uint64_t kd = sdesc_sw128(smem_u32(smem + Y::K), 16, 1024);
+    const uint64_t vd = sdesc_sw128(smem_u32(smem + Y::V), 16, 1024);
+    const uint64_t qd = sdesc_sw128(smem_u32(smem + Y::Q), 16, 1024);
+    const uint64_t dd = sdesc_sw128(smem_u32(smem + Y::D), 16, 1024);
+    const uint64_t qd_mn = sdesc_sw128(smem_u32(smem + Y::Q), HALF_BYTES, 1024);
+    const uint64_t dd_mn = sdesc_sw128(smem_u32(smem + Y::D), HALF_BYTES, 1024);
+    constexpr uint64_t ST = TILE_BYTES >> 4;
+    bool ok = mbar_wait_warp(kv_full, 0) && mbar_wait_warp(&q_full[0], 0);
+    if (ok) {
+      tc_fence_after();
+      mma_abt(tmem, kd, qd);
+      umma_commit(s_full);
+      ok = mbar_wait_warp(&d_full[0], 0);
+      if (ok) {
+        tc_fence_after();
+        mma_abt(tmem + 128, vd, dd);
+        umma_commit(dp_full);
+      }
+    }
+    for (int i = 0; i < n_q && ok; ++i) {
+      const bool more = i + 1 < n_q;
+      const uint64_t cur = (uint64_t)(i & 1) * ST, nxt = (uint64_t)((i + 1) & 1) * ST;
+      const uint32_t nph = ((i + 1) >> 1) & 1;
+      // Q(i + 1) was requested a step ago; waited for off the P -> dV path
+      ok = (!more || mbar_wait_warp(&q_full[(i + 1) & 1], nph)) && mbar_wait_warp(p_ready, i & 1);
+      if (!ok) break;
+      tc_fence_after();
+      mma_tmem_ab(tmem + 256, tmem, dd_mn + cur, i != 0);
+      umma_commit(&d_empty[i & 1]);
+      if (more) {
+        mma_abt(tmem, kd, qd + nxt);
+        umma_commit(s_full);
+        ok = mbar_wait_warp(&d_full[(i + 1) & 1], nph);
+      }
+      ok = ok && mbar_wait_warp(ds_ready, i & 1);
+      if (!ok) break;
+      tc_fence_after();
+      mma_tmem_ab(tmem + 384, tmem + 128, qd_mn + cur, i != 0);
+      umma_commit(&q_empty[i & 1]);
+      if (more) {
+        mma_abt(tmem + 128, vd, dd + nxt);
+        umma_commit(dp_full);
+      }
+    }
+    umma_commit(acc_full);
+    drain_mmas(drain);
+  } else {
+    const int qw = warp & 3, g = (warp - 2) >> 2;  // TMEM lane quarter, 32-column group
+    const int r = qw * 32 + lane;                  // key row of the tile
+    const uint32_t lanes = (uint32_t)(qw * 32) << 16;
+    const uint32_t tS = tmem + lanes + g * 32, tP = tS + 128;
+    const uint64_t sc2 = f2_pack(scale_log2, scale_log2);
+    bool ok = true;
+    for (int i = 0; i < n_q; ++i) {
+      const float* st = reinterpret_cast<const float*>(smem + Y::STAT + (i & 1) * 1024) + g * 32;
+      ok = mbar_wait_warp(&q_full[i & 1], (i >> 1) & 1) && mbar_wait_warp(s_full, i & 1);
+      if (!ok) break;
+      tc_fence_after();
+      float p[32];
+      uint32_t pk[16];
+      tmem_ld32(tS, reinterpret_cast<uint32_t*>(p));
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 32; c += 4) {
+        const float4 nl = *reinterpret_cast<const float4*>(st + c);
+        float x0, x1, x2, x3;
+        f2_unpack(f2_fma(f2_pack(p[c], p[c + 1]), sc2, f2_pack(nl.x, nl.y)), x0, x1);
+        f2_unpack(f2_fma(f2_pack(p[c + 2], p[c + 3]), sc2, f2_pack(nl.z, nl.w)), x2, x3);
+        p[c] = ex2_approx(x0);
+        p[c + 1] = ex2_approx(x1);
+        p[c + 2] = ex2_approx(x2);
+        p[c + 3] = ex2_approx(x3);
+        pk[c / 2] = pack_bf16x2(p[c], p[c + 1]);
+        pk[c / 2 + 1] = pack_bf16x2(p[c + 2], p[c + 3]);
+      }
+      tmem_st16(tS, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_ready);
+      ok = mbar_wait_warp(dp_full, i & 1);
+      if (!ok) break;
+      tc_fence_after();
+      float dp[32];
+      tmem_ld32(tP, reinterpret_cast<uint32_t*>(dp));
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 32; c += 4) {
+        const float4 nd = *reinterpret_cast<const float4*>(st + 128 + c);
+        float a, b;
+        f2_unpack(f2_mul(f2_pack(p[c], p[c + 1]), f2_add(f2_pack(dp[c], dp[c + 1]), f2_pack(nd.x, nd.y))), a, b);
+        pk[c / 2] = pack_bf16x2(a, b);
+        f2_unpack(f2_mul(f2_pack(p[c + 2], p[c + 3]), f2_add(f2_pack(dp[c + 2], dp[c + 3]), f2_pack(nd.z, nd.w))), a, b);
+        pk[c / 2 + 1] = pack_bf16x2(a, b);
+      }
+      tmem_st16(tP, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_ready);
+    }
+    ok = ok && mbar_wait_warp(acc_full, 0);
+    if (ok) {
+      tc_fence_after();
+      // group 0, 1: the halves of dV; 2, 3: of dK
+      bf16* dst = (g < 2 ? dv : dk) + ((long)h * L_pad + key0 + r) * 128 + (g & 1) * 64;
+      const uint32_t src = tmem + lanes + 256 + g * 64;
+      const float sc = g < 2 ? 1.0f : scale;
+      const bool valid = key0 + r < L;
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        store_cols32(src + c * 32, sc, dst + c * 32);
+        if (!valid) zero_cols32(dst + c * 32);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------ dQ
+// TMEM: S(j) alternating in [0, 128) and [128, 256) (dS(j) over it), dP
+// [256, 384), dQ [384, 512).  After dS(j) is stored the tensor core runs
+// dP(j + 1), dQ(j), S(j + 2) while the exponentials of S(j + 1), taken a step
+// earlier, proceed.
+struct QLayout {
+  static constexpr int KS = 3;  // K stages: K(j) for dQ(j) while S(j + 2) reads K(j + 2)
+  static constexpr int Q = 0, D = TILE_BYTES, K = 2 * TILE_BYTES, V = K + KS * TILE_BYTES;
+  static constexpr int BAR = V + 2 * TILE_BYTES;
+  static constexpr int BYTES = BAR + 256 + 1024;
+  static_assert(BYTES <= 232448, "shared memory per CTA");
+};
+
+__global__ void __launch_bounds__(THREADS, 1)
+    attention_bwd_q_kernel(const __grid_constant__ BwdMaps maps, const float* __restrict__ nlse2,
+                           const float* __restrict__ ndelta, int L, int L_pad, float scale, float scale_log2,
+                           bf16* __restrict__ dq) {
+  using Y = QLayout;
+  constexpr int KS = Y::KS;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Y::BAR);
+  uint64_t* q_full = bars + 0;   // Q and dO
+  uint64_t* k_full = bars + 1;   // [3]
+  uint64_t* k_empty = bars + 4;  // [3] after dQ of the tile
+  uint64_t* v_full = bars + 7;   // [2]
+  uint64_t* v_empty = bars + 9;  // [2] after dP of the tile
+  uint64_t* s_full = bars + 11;  // [2] per S buffer
+  uint64_t* dp_full = bars + 13;
+  uint64_t* ds_ready = bars + 14;
+  uint64_t* acc_full = bars + 15;
+  uint64_t* drain = bars + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 17);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int row0 = blockIdx.x * TILE, h = blockIdx.y;
+  const int n_k = (L + TILE - 1) / TILE;
+  if (row0 >= L) {  // a tile of padding rows
+    for (int i = threadIdx.x; i < TILE * 16; i += THREADS)
+      reinterpret_cast<uint4*>(dq)[((long)h * L_pad + row0 + (i >> 4)) * 16 + (i & 15)] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < KS; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+      mbar_init(&s_full[s], 1);
+    }
+    mbar_init(dp_full, 1);
+    mbar_init(ds_ready, CWARPS);
+    mbar_init(acc_full, 1);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(q_full, 2 * TILE_BYTES);
+      load_head_tile(smem + Y::Q, &maps.q, q_full, row0, h);
+      load_token_tile(smem + Y::D, &maps.d, q_full, row0, h);
+      long long k_issued = 0, v_issued = 0;
+      for (int j = 0; j < n_k; ++j) {
+        const int sk = j % KS, sv = j & 1;
+        if (!mbar_wait(&k_empty[sk], ((j / KS) & 1) ^ 1)) break;
+        mbar_arrive_expect_tx(&k_full[sk], TILE_BYTES);
+        load_head_tile(smem + Y::K + sk * TILE_BYTES, &maps.k, &k_full[sk], j * TILE, h);
+        ++k_issued;
+        if (!mbar_wait(&v_empty[sv], ((j >> 1) & 1) ^ 1)) break;
+        mbar_arrive_expect_tx(&v_full[sv], TILE_BYTES);
+        load_head_tile(smem + Y::V + sv * TILE_BYTES, &maps.v, &v_full[sv], j * TILE, h);
+        ++v_issued;
+      }
+      mbar_wait(q_full, 0);
+      drain_loads(k_full, KS, k_issued);
+      drain_loads(v_full, 2, v_issued);
+    }
+  } else if (warp == 1) {
+    const uint64_t qd = sdesc_sw128(smem_u32(smem + Y::Q), 16, 1024);
+    const uint64_t dd = sdesc_sw128(smem_u32(smem + Y::D), 16, 1024);
+    const uint64_t kd = sdesc_sw128(smem_u32(smem + Y::K), 16, 1024);
+    const uint64_t vd = sdesc_sw128(smem_u32(smem + Y::V), 16, 1024);
+    const uint64_t kd_mn = sdesc_sw128(smem_u32(smem + Y::K), HALF_BYTES, 1024);
+    constexpr uint64_t ST = TILE_BYTES >> 4;
+    auto issue_s = [&](int j) {  // S(j) into its buffer
+      if (!mbar_wait_warp(&k_full[j % KS], (j / KS) & 1)) return false;
+      tc_fence_after();
+      mma_abt(tmem + (j & 1) * 128, qd, kd + (uint64_t)(j % KS) * ST);
+      umma_commit(&s_full[j & 1]);
+      return true;
+    };
+    auto issue_dp = [&](int j) {
+      if (!mbar_wait_warp(&v_full[j & 1], (j >> 1) & 1)) return false;
+      tc_fence_after();
+      mma_abt(tmem + 256, dd, vd + (uint64_t)(j & 1) * ST);
+      umma_commit(dp_full);
+      umma_commit(&v_empty[j & 1]);
+      return true;
+    };
+    bool ok = mbar_wait_warp(q_full, 0) && issue_s(0) && issue_dp(0) && (n_k < 2 || issue_s(1));
+    for (int j = 0; j < n_k && ok; ++j) {
+      if (!mbar_wait_warp(ds_ready, j & 1)) { ok = false; break; }
+      tc_fence_after();
+      if (j + 1 < n_k && !issue_dp(j + 1)) { ok = false; break; }
+      mma_tmem_ab(tmem + 384, tmem + (j & 1) * 128, kd_mn + (uint64_t)(j % KS) * ST, j != 0);
+      umma_commit(&k_empty[j % KS]);
+      if (j + 2 < n_k && !issue_s(j + 2)) { ok = false; break; }
+    }
+    umma_commit(acc_full);
+    drain_mmas(drain);
+  } else {
+    const int qw = warp & 3, g = (warp - 2) >> 2;
+    const int r = qw * 32 + lane;  // query row of the tile
+    const uint32_t lanes = (uint32_t)(qw * 32) << 16;
+    const uint32_t tP = tmem + lanes + 256 + g * 32;
+    const float nl = nlse2[(long)h * L_pad + row0 + r], nd = ndelta[(long)h * L_pad + row0 + r];
+    const uint64_t sc2 = f2_pack(scale_log2, scale_log2), nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
+    bool ok = true;
+    for (int j = 0; j < n_k; ++j) {
+      const uint32_t tS = tmem + lanes + (j & 1) * 128 + g * 32;
+      ok = mbar_wait_warp(&s_full[j & 1], (j >> 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      float p[32], dp[32];
+      tmem_ld32(tS, reinterpret_cast<uint32_t*>(p));
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        float x0, x1;
+        f2_unpack(f2_fma(f2_pack(p[c], p[c + 1]), sc2, nl2), x0, x1);
+        p[c] = ex2_approx(x0);
+        p[c + 1] = ex2_approx(x1);
+      }
+      const int valid = L - j * TILE - g * 32;
+      if (valid < 32) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (c >= valid) p[c] = 0.f;
+      }
+      ok = mbar_wait_warp(dp_full, j & 1);
+      if (!ok) break;
+      tc_fence_after();
+      tmem_ld32(tP, reinterpret_cast<uint32_t*>(dp));
+      tmem_wait_ld();
+      uint32_t pk[16];
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        float a, b;
+        f2_unpack(f2_mul(f2_pack(p[c], p[c + 1]), f2_add(f2_pack(dp[c], dp[c + 1]), nd2)), a, b);
+        pk[c / 2] = pack_bf16x2(a, b);
+      }
+      tmem_st16(tS, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_ready);
+    }
+    ok = ok && mbar_wait_warp(acc_full, 0);
+    if (ok) {
+      tc_fence_after();
+      bf16* dst = dq + ((long)h * L_pad + row0 + r) * 128 + g * 32;
+      store_cols32(tmem + lanes + 384 + g * 32, scale, dst);
+      if (row0 + r >= L) zero_cols32(dst);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// [H][L_pad][128] heads as 64 x 128-row boxes whose rows end at L
+bool make_tmap_heads(CUtensorMap* map, const void* base, int H, int L, int L_pad) {
+  gemm_detail::EncodeTiledFn fn = gemm_detail::encode_fn();
+  if (!fn) return false;
+  cuuint64_t gdim[3] = {128, (cuuint64_t)L, (cuuint64_t)H};
+  cuuint64_t gstride[2] = {256, (cuuint64_t)L_pad * 256};
+  cuuint32_t box[3] = {64, 128, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), gdim, gstride, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace attn_bwd
+
+// ws: nlse2 and ndelta, [H][L_pad] fp32 each
+cudaError_t launch_attention_bwd(const bf16* q, const bf16* k, const bf16* v, const bf16* o, const float* lse,
+                                 const bf16* d, int H, int L, int L_pad, float scale, float scale_log2, bf16* dq,
+                                 bf16* dk, bf16* dv, float* ws, cudaStream_t stream) {
+  using namespace attn_bwd;
+  static unsigned long long kv_done = 0, q_done = 0;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(attention_bwd_kv_kernel), KvLayout::BYTES, &kv_done);
+  if (e != cudaSuccess) return e;
+  e = ensure_smem_attr(reinterpret_cast<const void*>(attention_bwd_q_kernel), QLayout::BYTES, &q_done);
+  if (e != cudaSuccess) return e;
+  BwdMaps maps;
+  if (!make_tmap_heads(&maps.q, q, H, L, L_pad) || !make_tmap_heads(&maps.k, k, H, L, L_pad) ||
+      !make_tmap_heads(&maps.v, v, H, L, L_pad) || !make_tmap_bf16(&maps.d, d, L, 128L * H, 128L * H, 128))
+    return cudaErrorInvalidValue;
+  float* nlse2 = ws;
+  float* ndelta = ws + (size_t)H * L_pad;
+  const long pieces = (long)L_pad * H * 16;
+  const long blocks = (pieces + 255) / 256, most = (long)num_sms() * 16;
+  attention_delta_kernel<<<(int)(blocks < most ? blocks : most), 256, 0, stream>>>(o, d, lse, H, L, L_pad, nlse2,
+                                                                                   ndelta);
+  const dim3 grid(L_pad / attn_detail::TILE, H);
+  attention_bwd_kv_kernel<<<grid, THREADS, KvLayout::BYTES, stream>>>(maps, nlse2, ndelta, L, L_pad, scale, scale_log2,
+                                                                      dk, dv);
+  attention_bwd_q_kernel<<<grid, THREADS, QLayout::BYTES, stream>>>(maps, nlse2, ndelta, L, L_pad, scale, scale_log2,
+                                                                    dq);
+  return cudaGetLastError();
+}
+
+}  // namespace h3

@@ -519,6 +519,7 @@ __global__ void __launch_bounds__(SLayout<QK8, PRO>::THREADS, 1)
         }
       } else {
         const float inv = (grow < L) ? 1.0f / l : 0.0f;
+        if (out.lse && hf == 0) out.lse[(long)h * L_pad + grow] = grow < L ? (B + log2f(l)) * 0.693147181f : 0.f;
         bf16* dst = sentinel_ptr(out, grow, h);
         // this warp writes O columns [64 hf, 64 hf + 64) of its row
 #pragma unroll 1

@@ -103,6 +103,7 @@ struct AttnOut {
   long ld;
   int head0, L_shard;
   bf16* shard[8];
+  float* lse;  // [H][L_pad] log-sum-exp of each row's scores, or null
 };
 
 // RMSNorm + 3-D RoPE taken in the attention prologue (split kernel, PRO):
@@ -471,6 +472,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tc_fence_after();
       const int grow = qt * TILE + r;
       const float inv = (grow < L) ? 1.0f / l_sum : 0.0f;
+      if (out.lse) out.lse[(long)h * L_pad + grow] = grow < L ? (m_ref + log2f(l_sum)) * 0.693147181f : 0.f;
       const int owner = grow / out.L_shard;
       bf16* dst = out.shard[owner] + (long)(grow - owner * out.L_shard) * out.ld + (out.head0 + h) * 128;
 #pragma unroll 1
@@ -546,6 +548,7 @@ cudaError_t launch_attention(const AttnProblem& p, cudaStream_t stream) {
     out.head0 = 0;
     out.L_shard = p.L_pad;
     out.shard[0] = p.o;
+    out.lse = p.lse;
   }
   dim3 grid((n_qt + 1) / 2, p.H);
 #ifndef H3_ATTN_SPLIT

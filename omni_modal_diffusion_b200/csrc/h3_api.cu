@@ -653,3 +653,4 @@ int h3_set_wait_limit_ns(uint64_t ns) {
 #include "h3_fp8.cu"
 #include "h3_sp.cu"
 #include "h3_noalloc.cu"
+#include "h3_bwd.cu"

@@ -106,6 +106,9 @@ struct AttnProblem {
   int sp_n, sp_L_shard, sp_head0;
   long sp_ld;
   bf16* sp_o[8];
+  // lse (may be null): [H][L_pad] fp32, log(sum_j exp(score_ij)) of every
+  // valid query row, 0 in padding rows; not with prologue or sp_n
+  float* lse;
   // qk8: q, k hold e4m3 codes (one byte per element) written by the QKV
   // epilogue with qk_e4m3; qn_w, kn_w give their scales
   int qk8;

@@ -34,7 +34,10 @@ EXPORTS = (
     "h3_ffn_e4m3_workspace_bytes", "h3_ffn_swiglu_e4m3", "h3_block_forward_e4m3",
     "h3_sp_make_layout", "h3_qkv_qknorm_mrope_sp", "h3_qkv_qknorm_mrope_sp_e4m3", "h3_attention_sp",
     "h3_text_refine",
+    "h3_backward_workspace_bytes", "h3_adaln_norm_modulate_backward", "h3_qkv_qknorm_mrope_backward",
+    "h3_attention_lse", "h3_attention_backward", "h3_gated_residual_backward", "h3_ffn_swiglu_backward",
 )
+H3_BWD_ADALN, H3_BWD_QKV, H3_BWD_ATTENTION, H3_BWD_GATED_RESIDUAL, H3_BWD_FFN = range(5)
 H3_SP_MAX_RANKS = 8
 H3_FFN_STATIC_WS_BYTES = 32 * 1024 * 1024
 
@@ -139,6 +142,13 @@ def lib() -> ctypes.CDLL:
             "h3_attention_sp": (ci, [pd, ctypes.POINTER(SPLayout), ctypes.POINTER(SPPeers), vp, vp, ci, vp]),
             "h3_text_refine": (ci, [pd, pr, vp, ci, ctypes.POINTER(ctypes.c_void_p), vp,
                                     ctypes.POINTER(BlockWeights), ctypes.POINTER(BlockBuffers), ci, vp]),
+            "h3_backward_workspace_bytes": (ctypes.c_size_t, [pd, ci, ci]),
+            "h3_adaln_norm_modulate_backward": (ci, [pd, pr, vp, vp, ci, vp, vp, vp, vp, vp, vp]),
+            "h3_qkv_qknorm_mrope_backward": (ci, [pd, pr] + [vp] * 14),
+            "h3_attention_lse": (ci, [pd, pr] + [vp] * 8),
+            "h3_attention_backward": (ci, [pd, pr] + [vp] * 11),
+            "h3_gated_residual_backward": (ci, [pd, pr, vp, vp, vp, vp, ci, vp, vp, vp, vp, vp]),
+            "h3_ffn_swiglu_backward": (ci, [pd, pr] + [vp] * 11),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -461,3 +471,102 @@ def h3_text_refine(dims, ranges, x, mods: list, pos, weights: list, buffers: Blo
     w_arr = (BlockWeights * max(n, 1))(*weights)
     _check(lib().h3_text_refine(ctypes.byref(dims), ctypes.byref(ranges), _ptr(x, F32, "x"), n, mod_ptrs,
                                 _ptr(pos, F32, "pos"), w_arr, ctypes.byref(buffers), flags, _stream(stream)))
+
+
+# ------------------------------------------------------------ backward pass
+
+def h3_backward_workspace_bytes(dims, L_pad: int, op: int) -> int:
+    return int(lib().h3_backward_workspace_bytes(ctypes.byref(dims), L_pad, op))
+
+
+def _call_backward(name, dims, ranges, op, tensors, stream, ints=()):
+    """One backward call: tensors is a list of (name, tensor, dtype, numel or
+    None, optional) in the order of the C arguments, ints {position: value} the
+    plain arguments among them.  Sizes are checked here, where they are known:
+    the C call sees only pointers.  The call runs on the tensors' device, on
+    `stream` or that device's current stream."""
+    dev = None
+    for n, t, dt, count, optional in tensors:
+        if t is None:
+            if optional:
+                continue
+            raise TypeError(f"{n} must be a CUDA tensor")
+        _ptr(t, dt, n)
+        if count is not None and t.numel() != count:
+            raise ValueError(f"{n} must have {count} elements, got {t.numel()}")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{n} is on {t.device}, the others on {dev}")
+    if op is not None:
+        ws = tensors[-1][1]
+        need = h3_backward_workspace_bytes(dims, ranges.L_pad, op)
+        if ws.numel() * ws.element_size() < need:
+            raise ValueError(f"workspace too small: {need} bytes needed")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    args = [_ptr(t) for _, t, _, _, _ in tensors]
+    for at, v in sorted(dict(ints).items()):
+        args.insert(at, v)
+    with torch.cuda.device(dev):
+        _check(getattr(lib(), name)(ctypes.byref(dims), ctypes.byref(ranges), *args, _stream(stream)))
+
+
+def h3_adaln_norm_modulate_backward(dims, ranges, x, mod, branch, dxm, dres, dx, dmod, ws, stream=None):
+    """dx = dres + the gradient through the norm and modulation (dx may be
+    dres); dmod [3][6][D] bf16 or None: the branch's shift and scale slots."""
+    n = ranges.L_pad * dims.D
+    _call_backward("h3_adaln_norm_modulate_backward", dims, ranges, H3_BWD_ADALN,
+                   [("x", x, F32, n, False), ("mod", mod, F32, 18 * dims.D, False), ("dxm", dxm, BF16, n, False),
+                    ("dres", dres, F32, n, False), ("dx", dx, F32, n, False), ("dmod", dmod, BF16, 18 * dims.D, True),
+                    ("ws", ws, U8, None, False)], stream, {2: branch})
+
+
+def h3_qkv_qknorm_mrope_backward(dims, ranges, xm, Wqkv, qn_w, kn_w, pos, dq, dk, dv, dxm, dWqkv, dqn_w, dkn_w, ws,
+                                 stream=None):
+    """dWqkv, dqn_w, dkn_w may be None (frozen weights)."""
+    n, h, w = ranges.L_pad * dims.D, ranges.L_pad * dims.I, 3 * dims.I * dims.D
+    _call_backward("h3_qkv_qknorm_mrope_backward", dims, ranges, H3_BWD_QKV,
+                   [("xm", xm, BF16, n, False), ("Wqkv", Wqkv, BF16, w, False), ("qn_w", qn_w, BF16, 128, False),
+                    ("kn_w", kn_w, BF16, 128, False), ("pos", pos, F32, ranges.L_pad * 3, False),
+                    ("dq", dq, BF16, h, False), ("dk", dk, BF16, h, False), ("dv", dv, BF16, h, False),
+                    ("dxm", dxm, BF16, n, False), ("dWqkv", dWqkv, BF16, w, True), ("dqn_w", dqn_w, BF16, 128, True),
+                    ("dkn_w", dkn_w, BF16, 128, True), ("ws", ws, U8, None, False)], stream)
+
+
+def h3_attention_lse(dims, ranges, q, k, v, o, lse, qn_w=None, kn_w=None, stream=None):
+    """h3_attention on normalised and rotated q, k, which also writes each
+    row's log-sum-exp, lse [H][L_pad] fp32."""
+    h = ranges.L_pad * dims.I
+    _call_backward("h3_attention_lse", dims, ranges, None,
+                   [("q", q, BF16, h, False), ("k", k, BF16, h, False), ("v", v, BF16, h, False),
+                    ("qn_w", qn_w, BF16, 128, True), ("kn_w", kn_w, BF16, 128, True), ("o", o, BF16, h, False),
+                    ("lse", lse, F32, dims.H * ranges.L_pad, False)], stream)
+
+
+def h3_attention_backward(dims, ranges, q, k, v, o, lse, do, dq, dk, dv, ws, stream=None):
+    h = ranges.L_pad * dims.I
+    _call_backward("h3_attention_backward", dims, ranges, H3_BWD_ATTENTION,
+                   [(n, t, BF16, h, False) for n, t in (("q", q), ("k", k), ("v", v), ("o", o))]
+                   + [("lse", lse, F32, dims.H * ranges.L_pad, False)]
+                   + [(n, t, BF16, h, False) for n, t in (("do", do), ("dq", dq), ("dk", dk), ("dv", dv))]
+                   + [("ws", ws, U8, None, False)], stream)
+
+
+def h3_gated_residual_backward(dims, ranges, dx, o, Wo, mod, do, dWo, dmod, ws, branch=H3_MSA, stream=None):
+    """dWo, dmod may be None; dmod: the branch's gate slot."""
+    h, w = ranges.L_pad * dims.I, dims.D * dims.I
+    _call_backward("h3_gated_residual_backward", dims, ranges, H3_BWD_GATED_RESIDUAL,
+                   [("dx", dx, F32, ranges.L_pad * dims.D, False), ("o", o, BF16, h, False), ("Wo", Wo, BF16, w, False),
+                    ("mod", mod, F32, 18 * dims.D, False), ("do", do, BF16, h, False), ("dWo", dWo, BF16, w, True),
+                    ("dmod", dmod, BF16, 18 * dims.D, True), ("ws", ws, U8, None, False)], stream, {4: branch})
+
+
+def h3_ffn_swiglu_backward(dims, ranges, dx, xm, Wgu, Wd, mod, dxm, dWgu, dWd, dmod, ws, stream=None):
+    """dWgu, dWd, dmod may be None; dmod: the gate_mlp slot."""
+    n, w = ranges.L_pad * dims.D, dims.D * dims.F
+    _call_backward("h3_ffn_swiglu_backward", dims, ranges, H3_BWD_FFN,
+                   [("dx", dx, F32, n, False), ("xm", xm, BF16, n, False), ("Wgu", Wgu, BF16, 2 * w, False),
+                    ("Wd", Wd, BF16, w, False), ("mod", mod, F32, 18 * dims.D, False), ("dxm", dxm, BF16, n, False),
+                    ("dWgu", dWgu, BF16, 2 * w, True), ("dWd", dWd, BF16, w, True),
+                    ("dmod", dmod, BF16, 18 * dims.D, True), ("ws", ws, U8, None, False)], stream)

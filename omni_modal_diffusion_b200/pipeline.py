@@ -268,3 +268,73 @@ class H3Sampler:
         st = self.st
         per_block = (9 if self.e4m3 else 7) + 1  # attention: split kernel + fixup launch
         return st.launches_per_step() - 8 + per_block * self.n_layers
+
+
+class H3BlockTrain:
+    """One block with its backward pass, for fine-tuning the trunk on one GPU.
+
+    forward() runs the block on x in place and keeps what the backward pass
+    needs of it: x before each branch, q, k, v, o and the rows' log-sum-exp.
+    backward() takes the gradient of the block's output to that of its input
+    in place and returns the gradients of the weights and the modulation.  The
+    rest is recomputed.  Orchestration only, as in H3BlockStep; one workspace
+    serves every backward call, so forward and backward of one object run on
+    one stream at a time."""
+
+    WEIGHTS = ("Wqkv", "qn_w", "kn_w", "Wo", "Wgu", "Wd")
+
+    def __init__(self, dims, ranges, device="cuda"):
+        self.dims, self.ranges = dims, ranges
+        dev = self.device = torch.device(device)
+        Lp, D, I, F, H = ranges.L_pad, dims.D, dims.I, dims.F, dims.H
+        e = lambda *s, dt=torch.bfloat16: torch.empty(*s, dtype=dt, device=dev)
+        self.x0, self.x1 = e(Lp, D, dt=torch.float32), e(Lp, D, dt=torch.float32)
+        self.q, self.k, self.v = (e(H, Lp, 128) for _ in range(3))
+        self.o, self.lse = e(Lp, I), e(H, Lp, dt=torch.float32)
+        self.xm, self.dxm = e(Lp, D), e(Lp, D)
+        self.do = e(Lp, I)
+        self.dq, self.dk, self.dv = (e(H, Lp, 128) for _ in range(3))
+        need = max(h3.h3_backward_workspace_bytes(dims, Lp, op)
+                   for op in (h3.H3_BWD_ADALN, h3.H3_BWD_QKV, h3.H3_BWD_ATTENTION, h3.H3_BWD_GATED_RESIDUAL,
+                              h3.H3_BWD_FFN))
+        self.ws = e(max(need, 2 * Lp * F), dt=torch.uint8)
+
+    def forward(self, x, mod, pos, W, stream=None):
+        """x fp32 [L_pad][D], updated in place (the same values as
+        h3_block_forward's); mod [3][6][D]; W: the block's weights by name."""
+        d, r = self.dims, self.ranges
+        with torch.cuda.stream(stream or torch.cuda.current_stream(self.device)):
+            self.x0.copy_(x)
+            h3.h3_adaln_norm_modulate(d, r, x, mod, h3.H3_MSA, self.xm)
+            h3.h3_qkv_qknorm_mrope(d, r, self.xm, W["Wqkv"], W["qn_w"], W["kn_w"], pos, self.q, self.k, self.v)
+            h3.h3_attention_lse(d, r, self.q, self.k, self.v, self.o, self.lse, qn_w=W["qn_w"], kn_w=W["kn_w"])
+            h3.h3_gated_residual(d, r, x, self.o, W["Wo"], mod, h3.H3_MSA)
+            self.x1.copy_(x)
+            h3.h3_adaln_norm_modulate(d, r, x, mod, h3.H3_MLP, self.xm)
+            h3.h3_ffn_swiglu(d, r, x, self.xm, W["Wgu"], W["Wd"], mod, self.ws[:2 * r.L_pad * d.F].view(torch.bfloat16))
+
+    def backward(self, dx, mod, pos, W, frozen=(), stream=None) -> dict:
+        """dx fp32 [L_pad][D]: the gradient of the block's output, replaced by
+        that of its input.  Returns bf16 gradients by weight name and "mod"
+        ([3][6][D]); names in `frozen` are not computed."""
+        d, r = self.dims, self.ranges
+        unknown = set(frozen) - set(self.WEIGHTS) - {"mod"}
+        if unknown:
+            raise ValueError(f"unknown names in frozen: {sorted(unknown)}")
+        with torch.cuda.stream(stream or torch.cuda.current_stream(self.device)):
+            g = {n: torch.empty_like(W[n]) for n in self.WEIGHTS if n not in frozen}
+            if "mod" not in frozen:
+                g["mod"] = torch.empty(3, 6, d.D, dtype=torch.bfloat16, device=self.device)
+            dmod = g.get("mod")
+            h3.h3_adaln_norm_modulate(d, r, self.x1, mod, h3.H3_MLP, self.xm)
+            h3.h3_ffn_swiglu_backward(d, r, dx, self.xm, W["Wgu"], W["Wd"], mod, self.dxm, g.get("Wgu"), g.get("Wd"),
+                                      dmod, self.ws)
+            h3.h3_adaln_norm_modulate_backward(d, r, self.x1, mod, h3.H3_MLP, self.dxm, dx, dx, dmod, self.ws)
+            h3.h3_gated_residual_backward(d, r, dx, self.o, W["Wo"], mod, self.do, g.get("Wo"), dmod, self.ws)
+            h3.h3_attention_backward(d, r, self.q, self.k, self.v, self.o, self.lse, self.do, self.dq, self.dk,
+                                     self.dv, self.ws)
+            h3.h3_adaln_norm_modulate(d, r, self.x0, mod, h3.H3_MSA, self.xm)
+            h3.h3_qkv_qknorm_mrope_backward(d, r, self.xm, W["Wqkv"], W["qn_w"], W["kn_w"], pos, self.dq, self.dk,
+                                            self.dv, self.dxm, g.get("Wqkv"), g.get("qn_w"), g.get("kn_w"), self.ws)
+            h3.h3_adaln_norm_modulate_backward(d, r, self.x0, mod, h3.H3_MSA, self.dxm, dx, dx, dmod, self.ws)
+        return g
