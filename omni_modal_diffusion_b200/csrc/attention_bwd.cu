@@ -103,6 +103,33 @@ __device__ __forceinline__ void mma_tmem_ab(uint32_t d_tmem, uint32_t a_tmem, ui
                      (accumulate || kk != 0) ? 1u : 0u);
 }
 
+// 2^(s c + b) for a pair of scores, in place
+__device__ __forceinline__ void exp2_pair(float* s, uint64_t c2, uint64_t b2) {
+  float x0, x1;
+  f2_unpack(f2_fma(f2_pack(s[0], s[1]), c2, b2), x0, x1);
+  s[0] = ex2_approx(x0);
+  s[1] = ex2_approx(x1);
+}
+
+// 16 lanes x 32 consecutive 32-bit columns: thread t receives rows t / 4
+// (r[4i], r[4i + 1]) and t / 4 + 8 (r[4i + 2], r[4i + 3]) of columns 8i + 2 (t % 4)
+// and the next, i < 4.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// 16 lanes x 16 consecutive 32-bit columns: thread t gives rows t / 4 (r[2i])
+// and t / 4 + 8 (r[2i + 1]) of column 4i + t % 4: the bf16 pairs of the values
+// that tmem_ld_16x256b_x4 gave it.
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // 32 columns of one row of an fp32 accumulator, scaled, as bf16
 __device__ __forceinline__ void store_cols32(uint32_t taddr, float scale, bf16* dst) {
   float v[32];
@@ -120,15 +147,18 @@ __device__ __forceinline__ void zero_cols32(bf16* dst) {
 }
 
 // ------------------------------------------------------------ dK, dV
-// TMEM: S^T [0, 128) (P^T over it), dP^T [128, 256) (dS^T over it), dV, dK.
-// Tensor and elementwise work alternate between the two score tiles:
-//   exponentials of S^T(i)      while the tensor core runs dK(i - 1), dP^T(i)
-//   dS^T(i) from dP^T(i)        while it runs dV(i), S^T(i + 1)
+// TMEM: S^T [0, 128), dP^T [128, 256) with P^T and dS^T (bf16, half a column
+// each) over it, dV, dK.  S^T(i) is free as soon as it is in registers, so the
+// next one is taken while its exponentials run, and the tensor core's turn is
+//   dV(i) dK(i) dP^T(i + 1) S^T(i + 2)
+// of which only dV waits for the elementwise warps: P^T(i) is stored the
+// moment dP^T(i) has been read, while S^T(i + 1), already issued, runs.
 struct KvLayout {
-  static constexpr int K = 0, V = TILE_BYTES, Q = 2 * TILE_BYTES, D = 4 * TILE_BYTES;  // Q, dO: two stages
-  static constexpr int STAT = 6 * TILE_BYTES;  // [2][-lse log2 e, -delta][128]
+  static constexpr int QS = 3;  // Q stages: Q(i + 2) for S^T(i + 2) is loaded while dK(i) still reads Q(i)
+  static constexpr int K = 0, V = TILE_BYTES, Q = 2 * TILE_BYTES, D = Q + QS * TILE_BYTES;  // dO: two stages
+  static constexpr int STAT = D + 2 * TILE_BYTES;  // [2][-lse log2 e, -delta][128]
   static constexpr int BAR = STAT + 2 * 2 * 128 * 4;
-  static constexpr int BYTES = BAR + 256 + 1024;
+  static constexpr int BYTES = BAR + 256;
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
 
@@ -137,22 +167,27 @@ __global__ void __launch_bounds__(THREADS, 1)
                             const float* __restrict__ ndelta, int L, int L_pad, float scale, float scale_log2,
                             bf16* __restrict__ dk, bf16* __restrict__ dv) {
   using Y = KvLayout;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  constexpr int QS = Y::QS;
+  // seven tiles leave no room to align the base by hand: the swizzled tiles
+  // need 1 KB alignment, which the declaration asks for and the check below holds
+  extern __shared__ __align__(1024) uint8_t smem_kv[];
+  uint8_t* smem = smem_kv;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Y::BAR);
   uint64_t* kv_full = bars + 0;
-  uint64_t* q_full = bars + 1;    // [2] Q and its rows' statistics
-  uint64_t* q_empty = bars + 3;   // [2] after dK of the tile
-  uint64_t* d_full = bars + 5;    // [2]
-  uint64_t* d_empty = bars + 7;   // [2] after dV of the tile
-  uint64_t* s_full = bars + 9;
-  uint64_t* dp_full = bars + 10;
-  uint64_t* p_ready = bars + 11;
-  uint64_t* ds_ready = bars + 12;
-  uint64_t* acc_full = bars + 13;
-  uint64_t* drain = bars + 14;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
+  uint64_t* q_full = bars + 1;    // [3]
+  uint64_t* q_empty = bars + 4;   // [3] after dK of the tile
+  uint64_t* d_full = bars + 7;    // [2]
+  uint64_t* d_empty = bars + 9;   // [2] after dV of the tile
+  uint64_t* st_full = bars + 11;  // [2] the rows' statistics
+  uint64_t* st_empty = bars + 13; // [2] read by every elementwise warp
+  uint64_t* s_full = bars + 15;
+  uint64_t* s_read = bars + 16;   // S^T in registers
+  uint64_t* dp_full = bars + 17;
+  uint64_t* p_ready = bars + 18;
+  uint64_t* ds_ready = bars + 19;
+  uint64_t* acc_full = bars + 20;
+  uint64_t* drain = bars + 21;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 22);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int key0 = blockIdx.x * TILE, h = blockIdx.y;
   const int n_q = (L + TILE - 1) / TILE;
@@ -164,15 +199,24 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     return;
   }
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) atomicCAS(&g_h3_device_error, 0, 1);
+    return;
+  }
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < QS; ++s) {
       mbar_init(&q_full[s], 1);
       mbar_init(&q_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&d_full[s], 1);
       mbar_init(&d_empty[s], 1);
+      mbar_init(&st_full[s], 1);
+      mbar_init(&st_empty[s], CWARPS);
     }
     mbar_init(s_full, 1);
+    mbar_init(s_read, CWARPS);
     mbar_init(dp_full, 1);
     mbar_init(p_ready, CWARPS);
     mbar_init(ds_ready, CWARPS);
@@ -196,25 +240,29 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_arrive_expect_tx(kv_full, 2 * TILE_BYTES);
       load_head_tile(smem + Y::K, &maps.k, kv_full, key0, h);
       load_head_tile(smem + Y::V, &maps.v, kv_full, key0, h);
-      long long q_issued = 0, d_issued = 0;
+      long long q_issued = 0, st_issued = 0, d_issued = 0;
       for (int i = 0; i < n_q; ++i) {
-        const int st = i & 1;
+        const int sq = i % QS, st = i & 1;
         const uint32_t ph = ((i >> 1) & 1) ^ 1;
-        if (!mbar_wait(&q_empty[st], ph)) break;
-        mbar_arrive_expect_tx(&q_full[st], TILE_BYTES + 2 * 128 * 4);
-        load_head_tile(smem + Y::Q + st * TILE_BYTES, &maps.q, &q_full[st], i * TILE, h);
-        const long at = (long)h * L_pad + i * TILE;
-        bulk_load(smem + Y::STAT + st * 1024, nlse2 + at, 512, &q_full[st]);
-        bulk_load(smem + Y::STAT + st * 1024 + 512, ndelta + at, 512, &q_full[st]);
+        if (!mbar_wait(&q_empty[sq], ((i / QS) & 1) ^ 1)) break;
+        mbar_arrive_expect_tx(&q_full[sq], TILE_BYTES);
+        load_head_tile(smem + Y::Q + sq * TILE_BYTES, &maps.q, &q_full[sq], i * TILE, h);
         ++q_issued;
         if (!mbar_wait(&d_empty[st], ph)) break;
         mbar_arrive_expect_tx(&d_full[st], TILE_BYTES);
         load_token_tile(smem + Y::D + st * TILE_BYTES, &maps.d, &d_full[st], i * TILE, h);
         ++d_issued;
+        if (!mbar_wait(&st_empty[st], ph)) break;
+        mbar_arrive_expect_tx(&st_full[st], 2 * 128 * 4);
+        const long at = (long)h * L_pad + i * TILE;
+        bulk_load(smem + Y::STAT + st * 1024, nlse2 + at, 512, &st_full[st]);
+        bulk_load(smem + Y::STAT + st * 1024 + 512, ndelta + at, 512, &st_full[st]);
+        ++st_issued;
       }
       mbar_wait(kv_full, 0);
-      drain_loads(q_full, 2, q_issued);
+      drain_loads(q_full, QS, q_issued);
       drain_loads(d_full, 2, d_issued);
+      drain_loads(st_full, 2, st_issued);
     }
   } else if (warp == 1) {
     const uint64_t kd = sdesc_sw128(smem_u32(smem + Y::K), 16, 1024);
@@ -224,99 +272,110 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint64_t qd_mn = sdesc_sw128(smem_u32(smem + Y::Q), HALF_BYTES, 1024);
     const uint64_t dd_mn = sdesc_sw128(smem_u32(smem + Y::D), HALF_BYTES, 1024);
     constexpr uint64_t ST = TILE_BYTES >> 4;
-    bool ok = mbar_wait_warp(kv_full, 0) && mbar_wait_warp(&q_full[0], 0);
-    if (ok) {
+    auto issue_s = [&](int i) {
+      if (!mbar_wait_warp(&q_full[i % QS], (i / QS) & 1)) return false;
+      if (i > 0 && !mbar_wait_warp(s_read, (i - 1) & 1)) return false;
       tc_fence_after();
-      mma_abt(tmem, kd, qd);
+      mma_abt(tmem, kd, qd + (uint64_t)(i % QS) * ST);
       umma_commit(s_full);
-      ok = mbar_wait_warp(&d_full[0], 0);
-      if (ok) {
-        tc_fence_after();
-        mma_abt(tmem + 128, vd, dd);
-        umma_commit(dp_full);
-      }
-    }
+      return true;
+    };
+    auto issue_dp = [&](int i) {
+      if (!mbar_wait_warp(&d_full[i & 1], (i >> 1) & 1)) return false;
+      tc_fence_after();
+      mma_abt(tmem + 128, vd, dd + (uint64_t)(i & 1) * ST);
+      umma_commit(dp_full);
+      return true;
+    };
+    bool ok = mbar_wait_warp(kv_full, 0) && issue_s(0) && issue_dp(0) && (n_q < 2 || issue_s(1));
     for (int i = 0; i < n_q && ok; ++i) {
-      const bool more = i + 1 < n_q;
-      const uint64_t cur = (uint64_t)(i & 1) * ST, nxt = (uint64_t)((i + 1) & 1) * ST;
-      const uint32_t nph = ((i + 1) >> 1) & 1;
-      // Q(i + 1) was requested a step ago; waited for off the P -> dV path
-      ok = (!more || mbar_wait_warp(&q_full[(i + 1) & 1], nph)) && mbar_wait_warp(p_ready, i & 1);
-      if (!ok) break;
+      if (!mbar_wait_warp(p_ready, i & 1)) { ok = false; break; }
       tc_fence_after();
-      mma_tmem_ab(tmem + 256, tmem, dd_mn + cur, i != 0);
+      mma_tmem_ab(tmem + 256, tmem + 128, dd_mn + (uint64_t)(i & 1) * ST, i != 0);
       umma_commit(&d_empty[i & 1]);
-      if (more) {
-        mma_abt(tmem, kd, qd + nxt);
-        umma_commit(s_full);
-        ok = mbar_wait_warp(&d_full[(i + 1) & 1], nph);
-      }
-      ok = ok && mbar_wait_warp(ds_ready, i & 1);
-      if (!ok) break;
+      if (!mbar_wait_warp(ds_ready, i & 1)) { ok = false; break; }
       tc_fence_after();
-      mma_tmem_ab(tmem + 384, tmem + 128, qd_mn + cur, i != 0);
-      umma_commit(&q_empty[i & 1]);
-      if (more) {
-        mma_abt(tmem + 128, vd, dd + nxt);
-        umma_commit(dp_full);
-      }
+      mma_tmem_ab(tmem + 384, tmem + 128 + 16, qd_mn + (uint64_t)(i % QS) * ST, i != 0);
+      umma_commit(&q_empty[i % QS]);
+      ok = (i + 1 >= n_q || issue_dp(i + 1)) && (i + 2 >= n_q || issue_s(i + 2));
     }
     umma_commit(acc_full);
     drain_mmas(drain);
   } else {
     const int qw = warp & 3, g = (warp - 2) >> 2;  // TMEM lane quarter, 32-column group
-    const int r = qw * 32 + lane;                  // key row of the tile
+    const int r = qw * 32 + lane;                  // key row of the tile (epilogue)
     const uint32_t lanes = (uint32_t)(qw * 32) << 16;
     const uint32_t tS = tmem + lanes + g * 32, tP = tS + 128;
     const uint64_t sc2 = f2_pack(scale_log2, scale_log2);
     bool ok = true;
+    // The statistics belong to the columns (queries).  With one key row per
+    // thread a warp would read 32 + 32 of them for every thread, 1,024 clocks
+    // of the shared-memory pipe per tile (measured: 14% of the kernel); in the
+    // 16-lane layout a thread holds four rows of eight columns and reads 8 + 8.
     for (int i = 0; i < n_q; ++i) {
-      const float* st = reinterpret_cast<const float*>(smem + Y::STAT + (i & 1) * 1024) + g * 32;
-      ok = mbar_wait_warp(&q_full[i & 1], (i >> 1) & 1) && mbar_wait_warp(s_full, i & 1);
+      const float2* st = reinterpret_cast<const float2*>(smem + Y::STAT + (i & 1) * 1024) + g * 16 + (lane & 3);
+      ok = mbar_wait_warp(&st_full[i & 1], (i >> 1) & 1) && mbar_wait_warp(s_full, i & 1);
       if (!ok) break;
       tc_fence_after();
-      float p[32];
-      uint32_t pk[16];
-      tmem_ld32(tS, reinterpret_cast<uint32_t*>(p));
-      tmem_wait_ld();
+      float p[2][16];
+      uint32_t pk[2][8];
 #pragma unroll
-      for (int c = 0; c < 32; c += 4) {
-        const float4 nl = *reinterpret_cast<const float4*>(st + c);
-        float x0, x1, x2, x3;
-        f2_unpack(f2_fma(f2_pack(p[c], p[c + 1]), sc2, f2_pack(nl.x, nl.y)), x0, x1);
-        f2_unpack(f2_fma(f2_pack(p[c + 2], p[c + 3]), sc2, f2_pack(nl.z, nl.w)), x2, x3);
-        p[c] = ex2_approx(x0);
-        p[c + 1] = ex2_approx(x1);
-        p[c + 2] = ex2_approx(x2);
-        p[c + 3] = ex2_approx(x3);
-        pk[c / 2] = pack_bf16x2(p[c], p[c + 1]);
-        pk[c / 2 + 1] = pack_bf16x2(p[c + 2], p[c + 3]);
+      for (int hh = 0; hh < 2; ++hh)
+        tmem_ld_16x256b_x4(tS + ((uint32_t)(hh * 16) << 16), reinterpret_cast<uint32_t*>(p[hh]));
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_read);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float2 nl = st[c * 4];
+        const uint64_t nl2 = f2_pack(nl.x, nl.y);
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          exp2_pair(p[hh] + c * 4, sc2, nl2);
+          exp2_pair(p[hh] + c * 4 + 2, sc2, nl2);
+          pk[hh][c * 2] = pack_bf16x2(p[hh][c * 4], p[hh][c * 4 + 1]);
+          pk[hh][c * 2 + 1] = pack_bf16x2(p[hh][c * 4 + 2], p[hh][c * 4 + 3]);
+        }
       }
-      tmem_st16(tS, pk);
+      ok = mbar_wait_warp(dp_full, i & 1);
+      if (!ok) break;
+      tc_fence_after();
+      float dp[2][16];
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh)
+        tmem_ld_16x256b_x4(tP + ((uint32_t)(hh * 16) << 16), reinterpret_cast<uint32_t*>(dp[hh]));
+      tmem_wait_ld();
+      // the warp's own 32 columns of dP^T are read: P^T over the first 16
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) tmem_st_16x128b_x4(tP + ((uint32_t)(hh * 16) << 16), pk[hh]);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_ready);
-      ok = mbar_wait_warp(dp_full, i & 1);
-      if (!ok) break;
-      tc_fence_after();
-      float dp[32];
-      tmem_ld32(tP, reinterpret_cast<uint32_t*>(dp));
-      tmem_wait_ld();
 #pragma unroll
-      for (int c = 0; c < 32; c += 4) {
-        const float4 nd = *reinterpret_cast<const float4*>(st + 128 + c);
-        float a, b;
-        f2_unpack(f2_mul(f2_pack(p[c], p[c + 1]), f2_add(f2_pack(dp[c], dp[c + 1]), f2_pack(nd.x, nd.y))), a, b);
-        pk[c / 2] = pack_bf16x2(a, b);
-        f2_unpack(f2_mul(f2_pack(p[c + 2], p[c + 3]), f2_add(f2_pack(dp[c + 2], dp[c + 3]), f2_pack(nd.z, nd.w))), a, b);
-        pk[c / 2 + 1] = pack_bf16x2(a, b);
+      for (int c = 0; c < 4; ++c) {
+        const float2 nd = st[64 + c * 4];
+        const uint64_t nd2 = f2_pack(nd.x, nd.y);
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const int j = c * 4 + e;
+            float a, b;
+            f2_unpack(f2_mul(f2_pack(p[hh][j], p[hh][j + 1]), f2_add(f2_pack(dp[hh][j], dp[hh][j + 1]), nd2)), a, b);
+            pk[hh][c * 2 + e / 2] = pack_bf16x2(a, b);
+          }
       }
-      tmem_st16(tP, pk);
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) tmem_st_16x128b_x4(tP + 16 + ((uint32_t)(hh * 16) << 16), pk[hh]);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ds_ready);
+      if (lane == 0) {
+        mbar_arrive(ds_ready);
+        mbar_arrive(&st_empty[i & 1]);
+      }
     }
     ok = ok && mbar_wait_warp(acc_full, 0);
     if (ok) {
@@ -342,39 +401,52 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // ------------------------------------------------------------ dQ
-// TMEM: S(j) alternating in [0, 128) and [128, 256) (dS(j) over it), dP
-// [256, 384), dQ [384, 512).  After dS(j) is stored the tensor core runs
-// dP(j + 1), dQ(j), S(j + 2) while the exponentials of S(j + 1), taken a step
-// earlier, proceed.
+// TMEM: S(j) [0, 128), dP(j) [128, 256) with dS(j) over it, dQ [256, 384), and
+// Q and dO as bf16 A operands, [384, 448) and [448, 512): with both operands
+// in shared memory S and dP would read 128 KB of it a tile, with dQ's 32 KB and
+// the 64 KB that TMA writes 1,792 of its clocks against 1,536 of the tensor
+// core's.  As in the other kernel S(j) is free once it is in registers:
+//   dQ(j) dP(j + 1) S(j + 2)
+// of which dQ waits for dS(j).
 struct QLayout {
-  static constexpr int KS = 3;  // K stages: K(j) for dQ(j) while S(j + 2) reads K(j + 2)
-  static constexpr int Q = 0, D = TILE_BYTES, K = 2 * TILE_BYTES, V = K + KS * TILE_BYTES;
-  static constexpr int BAR = V + 2 * TILE_BYTES;
+  static constexpr int KS = 4, VS = 2;  // K stages: K(j) for dQ(j) while S(j + 2) reads K(j + 2)
+  static constexpr int K = 0, V = KS * TILE_BYTES;
+  static constexpr int BAR = V + VS * TILE_BYTES;
   static constexpr int BYTES = BAR + 256 + 1024;
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
 
+// D = A B^T over d = 128: A bf16 in TMEM, B a K-major 128 x 128 tile
+__device__ __forceinline__ void mma_tmem_abt(uint32_t d_tmem, uint32_t a_tmem, uint64_t bd) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    umma_bf16_tmem_a(d_tmem, a_tmem + kk * 8, bd + (uint64_t)(((kk >> 2) * HALF_BYTES + (kk & 3) * 32) >> 4), idesc,
+                     kk != 0 ? 1u : 0u);
+}
+
 __global__ void __launch_bounds__(THREADS, 1)
-    attention_bwd_q_kernel(const __grid_constant__ BwdMaps maps, const float* __restrict__ nlse2,
-                           const float* __restrict__ ndelta, int L, int L_pad, float scale, float scale_log2,
-                           bf16* __restrict__ dq) {
+    attention_bwd_q_kernel(const __grid_constant__ BwdMaps maps, const bf16* __restrict__ q, const bf16* __restrict__ d,
+                           const float* __restrict__ nlse2, const float* __restrict__ ndelta, int L, int L_pad, int H,
+                           float scale, float scale_log2, bf16* __restrict__ dq) {
   using Y = QLayout;
-  constexpr int KS = Y::KS;
+  constexpr int KS = Y::KS, VS = Y::VS;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Y::BAR);
-  uint64_t* q_full = bars + 0;   // Q and dO
-  uint64_t* k_full = bars + 1;   // [3]
-  uint64_t* k_empty = bars + 4;  // [3] after dQ of the tile
-  uint64_t* v_full = bars + 7;   // [2]
-  uint64_t* v_empty = bars + 9;  // [2] after dP of the tile
-  uint64_t* s_full = bars + 11;  // [2] per S buffer
-  uint64_t* dp_full = bars + 13;
-  uint64_t* ds_ready = bars + 14;
-  uint64_t* acc_full = bars + 15;
-  uint64_t* drain = bars + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 17);
+  uint64_t* q_ready = bars + 0;      // Q and dO in TMEM
+  uint64_t* k_full = bars + 1;       // [KS]
+  uint64_t* k_empty = k_full + KS;   // [KS] after dQ of the tile
+  uint64_t* v_full = k_empty + KS;   // [VS]
+  uint64_t* v_empty = v_full + VS;   // [VS] after dP of the tile
+  uint64_t* s_full = v_empty + VS;
+  uint64_t* s_read = s_full + 1;
+  uint64_t* dp_full = s_full + 2;
+  uint64_t* ds_ready = s_full + 3;
+  uint64_t* acc_full = s_full + 4;
+  uint64_t* drain = s_full + 5;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 6);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int row0 = blockIdx.x * TILE, h = blockIdx.y;
   const int n_k = (L + TILE - 1) / TILE;
@@ -384,16 +456,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     return;
   }
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
+    mbar_init(q_ready, CWARPS);
     for (int s = 0; s < KS; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < VS; ++s) {
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
-      mbar_init(&s_full[s], 1);
     }
+    mbar_init(s_full, 1);
+    mbar_init(s_read, CWARPS);
     mbar_init(dp_full, 1);
     mbar_init(ds_ready, CWARPS);
     mbar_init(acc_full, 1);
@@ -413,55 +486,49 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      mbar_arrive_expect_tx(q_full, 2 * TILE_BYTES);
-      load_head_tile(smem + Y::Q, &maps.q, q_full, row0, h);
-      load_token_tile(smem + Y::D, &maps.d, q_full, row0, h);
       long long k_issued = 0, v_issued = 0;
       for (int j = 0; j < n_k; ++j) {
-        const int sk = j % KS, sv = j & 1;
+        const int sk = j % KS, sv = j % VS;
         if (!mbar_wait(&k_empty[sk], ((j / KS) & 1) ^ 1)) break;
         mbar_arrive_expect_tx(&k_full[sk], TILE_BYTES);
         load_head_tile(smem + Y::K + sk * TILE_BYTES, &maps.k, &k_full[sk], j * TILE, h);
         ++k_issued;
-        if (!mbar_wait(&v_empty[sv], ((j >> 1) & 1) ^ 1)) break;
+        if (!mbar_wait(&v_empty[sv], ((j / VS) & 1) ^ 1)) break;
         mbar_arrive_expect_tx(&v_full[sv], TILE_BYTES);
         load_head_tile(smem + Y::V + sv * TILE_BYTES, &maps.v, &v_full[sv], j * TILE, h);
         ++v_issued;
       }
-      mbar_wait(q_full, 0);
       drain_loads(k_full, KS, k_issued);
-      drain_loads(v_full, 2, v_issued);
+      drain_loads(v_full, VS, v_issued);
     }
   } else if (warp == 1) {
-    const uint64_t qd = sdesc_sw128(smem_u32(smem + Y::Q), 16, 1024);
-    const uint64_t dd = sdesc_sw128(smem_u32(smem + Y::D), 16, 1024);
     const uint64_t kd = sdesc_sw128(smem_u32(smem + Y::K), 16, 1024);
     const uint64_t vd = sdesc_sw128(smem_u32(smem + Y::V), 16, 1024);
     const uint64_t kd_mn = sdesc_sw128(smem_u32(smem + Y::K), HALF_BYTES, 1024);
     constexpr uint64_t ST = TILE_BYTES >> 4;
-    auto issue_s = [&](int j) {  // S(j) into its buffer
+    auto issue_s = [&](int j) {
       if (!mbar_wait_warp(&k_full[j % KS], (j / KS) & 1)) return false;
+      if (j > 0 && !mbar_wait_warp(s_read, (j - 1) & 1)) return false;
       tc_fence_after();
-      mma_abt(tmem + (j & 1) * 128, qd, kd + (uint64_t)(j % KS) * ST);
-      umma_commit(&s_full[j & 1]);
+      mma_tmem_abt(tmem, tmem + 384, kd + (uint64_t)(j % KS) * ST);
+      umma_commit(s_full);
       return true;
     };
     auto issue_dp = [&](int j) {
-      if (!mbar_wait_warp(&v_full[j & 1], (j >> 1) & 1)) return false;
+      if (!mbar_wait_warp(&v_full[j % VS], (j / VS) & 1)) return false;
       tc_fence_after();
-      mma_abt(tmem + 256, dd, vd + (uint64_t)(j & 1) * ST);
+      mma_tmem_abt(tmem + 128, tmem + 448, vd + (uint64_t)(j % VS) * ST);
       umma_commit(dp_full);
-      umma_commit(&v_empty[j & 1]);
+      umma_commit(&v_empty[j % VS]);
       return true;
     };
-    bool ok = mbar_wait_warp(q_full, 0) && issue_s(0) && issue_dp(0) && (n_k < 2 || issue_s(1));
+    bool ok = mbar_wait_warp(q_ready, 0) && issue_s(0) && issue_dp(0) && (n_k < 2 || issue_s(1));
     for (int j = 0; j < n_k && ok; ++j) {
       if (!mbar_wait_warp(ds_ready, j & 1)) { ok = false; break; }
       tc_fence_after();
-      if (j + 1 < n_k && !issue_dp(j + 1)) { ok = false; break; }
-      mma_tmem_ab(tmem + 384, tmem + (j & 1) * 128, kd_mn + (uint64_t)(j % KS) * ST, j != 0);
+      mma_tmem_ab(tmem + 256, tmem + 128, kd_mn + (uint64_t)(j % KS) * ST, j != 0);
       umma_commit(&k_empty[j % KS]);
-      if (j + 2 < n_k && !issue_s(j + 2)) { ok = false; break; }
+      ok = (j + 1 >= n_k || issue_dp(j + 1)) && (j + 2 >= n_k || issue_s(j + 2));
     }
     umma_commit(acc_full);
     drain_mmas(drain);
@@ -469,25 +536,38 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int qw = warp & 3, g = (warp - 2) >> 2;
     const int r = qw * 32 + lane;  // query row of the tile
     const uint32_t lanes = (uint32_t)(qw * 32) << 16;
-    const uint32_t tP = tmem + lanes + 256 + g * 32;
+    const uint32_t tS = tmem + lanes + g * 32, tP = tS + 128;
+    {  // this warp's 32 of the row's 128 columns of Q and dO into TMEM
+      uint4 a[4], b[4];
+      const uint4* qs = reinterpret_cast<const uint4*>(q + ((long)h * L_pad + row0 + r) * 128) + g * 4;
+      const uint4* ds = reinterpret_cast<const uint4*>(d + (long)(row0 + r) * H * 128 + h * 128) + g * 4;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = row0 + r < L ? __ldg(qs + i) : make_uint4(0, 0, 0, 0);
+        b[i] = row0 + r < L ? __ldg(ds + i) : make_uint4(0, 0, 0, 0);
+      }
+      tmem_st16(tmem + lanes + 384 + g * 16, reinterpret_cast<const uint32_t*>(a));
+      tmem_st16(tmem + lanes + 448 + g * 16, reinterpret_cast<const uint32_t*>(b));
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_ready);
+    }
     const float nl = nlse2[(long)h * L_pad + row0 + r], nd = ndelta[(long)h * L_pad + row0 + r];
     const uint64_t sc2 = f2_pack(scale_log2, scale_log2), nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
     bool ok = true;
     for (int j = 0; j < n_k; ++j) {
-      const uint32_t tS = tmem + lanes + (j & 1) * 128 + g * 32;
-      ok = mbar_wait_warp(&s_full[j & 1], (j >> 1) & 1);
+      ok = mbar_wait_warp(s_full, j & 1);
       if (!ok) break;
       tc_fence_after();
       float p[32], dp[32];
       tmem_ld32(tS, reinterpret_cast<uint32_t*>(p));
       tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_read);
 #pragma unroll
-      for (int c = 0; c < 32; c += 2) {
-        float x0, x1;
-        f2_unpack(f2_fma(f2_pack(p[c], p[c + 1]), sc2, nl2), x0, x1);
-        p[c] = ex2_approx(x0);
-        p[c + 1] = ex2_approx(x1);
-      }
+      for (int c = 0; c < 32; c += 2) exp2_pair(p + c, sc2, nl2);
       const int valid = L - j * TILE - g * 32;
       if (valid < 32) {
 #pragma unroll
@@ -506,7 +586,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         f2_unpack(f2_mul(f2_pack(p[c], p[c + 1]), f2_add(f2_pack(dp[c], dp[c + 1]), nd2)), a, b);
         pk[c / 2] = pack_bf16x2(a, b);
       }
-      tmem_st16(tS, pk);
+      // the warp's own 32 columns of dP are read: dS over the first 16
+      tmem_st16(tP, pk);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -516,7 +597,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (ok) {
       tc_fence_after();
       bf16* dst = dq + ((long)h * L_pad + row0 + r) * 128 + g * 32;
-      store_cols32(tmem + lanes + 384 + g * 32, scale, dst);
+      store_cols32(tmem + lanes + 256 + g * 32, scale, dst);
       if (row0 + r >= L) zero_cols32(dst);
     }
   }
@@ -566,8 +647,8 @@ cudaError_t launch_attention_bwd(const bf16* q, const bf16* k, const bf16* v, co
   const dim3 grid(L_pad / attn_detail::TILE, H);
   attention_bwd_kv_kernel<<<grid, THREADS, KvLayout::BYTES, stream>>>(maps, nlse2, ndelta, L, L_pad, scale, scale_log2,
                                                                       dk, dv);
-  attention_bwd_q_kernel<<<grid, THREADS, QLayout::BYTES, stream>>>(maps, nlse2, ndelta, L, L_pad, scale, scale_log2,
-                                                                    dq);
+  attention_bwd_q_kernel<<<grid, THREADS, QLayout::BYTES, stream>>>(maps, q, d, nlse2, ndelta, L, L_pad, H, scale,
+                                                                    scale_log2, dq);
   return cudaGetLastError();
 }
 
