@@ -18,125 +18,169 @@ using ew_detail::range_of;
 //   dx       = dres + rstd (dh - mean(dh) - xhat mean(dh xhat))
 //   dshift_m = sum_{rows of m} dy,   dscale_m = sum_{rows of m} dy xhat
 // The statistics are recomputed from x (4 bytes of the 14 an element moves).
-// A CTA takes a run of rows of one modality and keeps its columns' two sums
-// in registers; they leave as one partial row per CTA.
-constexpr int AB_THREADS = 256;
+// A CTA takes a run of rows of one modality; its rows come through a ring of
+// shared-memory stages by bulk copies (x, dy and dres of a row, 10 D bytes),
+// so that HBM is never idle while a row waits for its two reductions, and its
+// columns' two sums stay in registers, leaving as one partial row per CTA.
+constexpr int AB_MAX_THREADS = 512;
+constexpr int AB_STAGES = 4;
+constexpr int AB_SMEM = 216 * 1024;  // per SM, for the stages of its CTAs
+
+struct AdalnPlan {
+  int threads;   // one float4 column each, up to 512; wider rows take several
+  int per_sm;    // CTAs per SM: narrow rows need several to keep enough bytes in flight
+  int stages;
+  int ctas;      // partial rows, at most
+};
+static AdalnPlan adaln_plan(int D) {
+  AdalnPlan p;
+  const int nv = D / 4;
+  p.threads = nv >= AB_MAX_THREADS ? AB_MAX_THREADS : (nv + 31) / 32 * 32;
+  p.per_sm = AB_MAX_THREADS / p.threads;
+  if (p.per_sm > 8) p.per_sm = 8;
+  const int fit = AB_SMEM / p.per_sm / (10 * D);
+  p.stages = fit < AB_STAGES ? fit : AB_STAGES;  // at least 2: 20 D <= 160 KB
+  p.ctas = 148 * p.per_sm;
+  return p;
+}
 
 struct Chunks {
   int first[4];   // CTAs [first[m], first[m + 1]) take modality m's rows
-  int rows[3];    // rows per CTA of modality m
+  int rows;       // rows per CTA
 };
 
-// N sums over the CTA at once; `red` holds N x 8 floats and is free again
-// after the call's last barrier plus the next call's first
+// N sums over the CTA at once; `red` holds N x 16 floats and is free again
+// after the next barrier
 template <int N>
 __device__ __forceinline__ void block_sums(float* v, float* red) {
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  const int w = threadIdx.x / 32, l = threadIdx.x % 32;
+  const int w = threadIdx.x / 32, l = threadIdx.x % 32, nw = blockDim.x / 32;
   if (l == 0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) red[i * 8 + w] = v[i];
+    for (int i = 0; i < N; ++i) red[i * 16 + w] = v[i];
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    float t = 0.f;
+    float t = l < nw ? red[i * 16 + l] : 0.f;
 #pragma unroll
-    for (int k = 0; k < AB_THREADS / 32; ++k) t += red[i * 8 + k];
-    v[i] = t;
+    for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    v[i] = __shfl_sync(0xffffffffu, t, 0);
   }
 }
 
-// VPT: float4 columns per thread (D <= 1024 VPT)
+__device__ __forceinline__ float4 unpack4(const uint2& g) {
+  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&g.x));
+  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&g.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// VPT: float4 columns per thread (D <= 4 VPT threads)
 template <int VPT>
-__global__ void __launch_bounds__(AB_THREADS) adaln_bwd_kernel(
+__global__ void __launch_bounds__(AB_MAX_THREADS) adaln_bwd_kernel(
     const float* __restrict__ x, const float* __restrict__ mod, int branch, const bf16* __restrict__ dy,
-    const float* dres, float* dx, RangeArgs rg, Chunks ch, int L, int L_pad, int D, float eps,
+    const float* dres, float* dx, RangeArgs rg, Chunks ch, int L, int L_pad, int D, float eps, int stages,
     float* __restrict__ part) {
-  __shared__ float red[2][3 * 8];
-  const int nv = D / 4;
+  extern __shared__ __align__(16) uint8_t smem_ab[];
+  __shared__ float red[2][3 * 16];
+  __shared__ uint64_t full[AB_STAGES];
+  const int nv = D / 4, T = blockDim.x;
   const int n_chunks = ch.first[3];
   if ((int)blockIdx.x >= n_chunks) {  // padding rows
     for (long row = L + blockIdx.x - n_chunks; row < L_pad; row += gridDim.x - n_chunks)
-      for (int i = threadIdx.x; i < nv; i += AB_THREADS)
+      for (int i = threadIdx.x; i < nv; i += T)
         reinterpret_cast<float4*>(dx + row * D)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     return;
   }
   const int m = (int)blockIdx.x >= ch.first[2] ? 2 : ((int)blockIdx.x >= ch.first[1] ? 1 : 0);
-  const int off = ((int)blockIdx.x - ch.first[m]) * ch.rows[m];
-  const int row_end = rg.start[m] + min(rg.count[m], off + ch.rows[m]);
+  const int off = ((int)blockIdx.x - ch.first[m]) * ch.rows;
+  const long row0 = rg.start[m] + off;
+  const int n_rows = min(rg.count[m] - off, ch.rows);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const uint32_t stage_bytes = 10u * D;
+  // row i's x | dres | dy into stage i % stages
+  auto load_row = [&](int i) {
+    const int st = i % stages;
+    uint8_t* dst = smem_ab + st * stage_bytes;
+    mbar_arrive_expect_tx(&full[st], stage_bytes);
+    bulk_load(dst, x + (row0 + i) * D, 4u * D, &full[st]);
+    bulk_load(dst + 4u * D, dres + (row0 + i) * D, 4u * D, &full[st]);
+    bulk_load(dst + 8u * D, dy + (row0 + i) * D, 2u * D, &full[st]);
+  };
+  if (threadIdx.x == 0)
+    for (int i = 0; i < stages - 1 && i < n_rows; ++i) load_row(i);
   const float4* scale = reinterpret_cast<const float4*>(mod + (long)(m * 6 + 3 * branch + 1) * D);
-  float4 a_shift[VPT], a_scale[VPT];
+  float4 a_shift[VPT], a_scale[VPT], sc[VPT];
 #pragma unroll
-  for (int k = 0; k < VPT; ++k) a_shift[k] = a_scale[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (long row = rg.start[m] + off; row < row_end; ++row) {
-    const float4* xr = reinterpret_cast<const float4*>(x + row * D);
-    const uint2* yr = reinterpret_cast<const uint2*>(dy + row * D);
-    const float4* rr = reinterpret_cast<const float4*>(dres + row * D);
+  for (int k = 0; k < VPT; ++k) {
+    const int i = threadIdx.x + k * T;
+    a_shift[k] = a_scale[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    sc[k] = i < nv ? __ldg(scale + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    sc[k] = make_float4(1.f + sc[k].x, 1.f + sc[k].y, 1.f + sc[k].z, 1.f + sc[k].w);
+  }
+  bool ok = true;
+  for (int r = 0; r < n_rows && ok; ++r) {
+    const int st = r % stages;
+    const float4* xr = reinterpret_cast<const float4*>(smem_ab + st * stage_bytes);
+    const float4* rr = xr + nv;
+    const uint2* yr = reinterpret_cast<const uint2*>(rr + nv);
+    ok = mbar_wait(&full[st], (r / stages) & 1);
     float4 v[VPT];
-    uint2 g[VPT];
     float s1[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int i = threadIdx.x + k * AB_THREADS;
+      const int i = threadIdx.x + k * T;
       v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      g[k] = make_uint2(0, 0);
-      if (i < nv) {
-        v[k] = __ldcs(xr + i);
-        g[k] = __ldcs(yr + i);
-        s1[0] += (v[k].x + v[k].y) + (v[k].z + v[k].w);
-      }
+      if (i < nv) v[k] = xr[i];
+      s1[0] += (v[k].x + v[k].y) + (v[k].z + v[k].w);
     }
     block_sums<1>(s1, red[0]);
+    // every thread has left row r - 1, whose stage takes row r + stages - 1
+    if (threadIdx.x == 0 && r + stages - 1 < n_rows) load_row(r + stages - 1);
     const float mu = s1[0] / (float)D;  // divided as the forward call divides: a constant row has xhat = 0
-    float s3[3] = {0.f, 0.f, 0.f};  // sum (x - mu)^2, sum dh, sum dh (x - mu)
+    float s3[3] = {0.f, 0.f, 0.f};      // sum (x - mu)^2, sum dh, sum dh (x - mu)
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int i = threadIdx.x + k * AB_THREADS;
+      const int i = threadIdx.x + k * T;
       if (i < nv) {
-        v[k].x -= mu;
-        v[k].y -= mu;
-        v[k].z -= mu;
-        v[k].w -= mu;
-        const float4 sc = __ldg(scale + i);
-        const float2 g0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&g[k].x));
-        const float2 g1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&g[k].y));
-        const float h0 = g0.x * (1.f + sc.x), h1 = g0.y * (1.f + sc.y), h2 = g1.x * (1.f + sc.z),
-                    h3 = g1.y * (1.f + sc.w);
+        v[k] = make_float4(v[k].x - mu, v[k].y - mu, v[k].z - mu, v[k].w - mu);
+        const float4 g = unpack4(yr[i]);
+        const float4 h = make_float4(g.x * sc[k].x, g.y * sc[k].y, g.z * sc[k].z, g.w * sc[k].w);
         s3[0] += (v[k].x * v[k].x + v[k].y * v[k].y) + (v[k].z * v[k].z + v[k].w * v[k].w);
-        s3[1] += (h0 + h1) + (h2 + h3);
-        s3[2] += (h0 * v[k].x + h1 * v[k].y) + (h2 * v[k].z + h3 * v[k].w);
+        s3[1] += (h.x + h.y) + (h.z + h.w);
+        s3[2] += (h.x * v[k].x + h.y * v[k].y) + (h.z * v[k].z + h.w * v[k].w);
       }
     }
     block_sums<3>(s3, red[1]);
     const float rstd = rsqrtf(s3[0] / (float)D + eps);
     const float mean_h = s3[1] / (float)D, mean_hx = s3[2] / (float)D * rstd;  // mean(dh), mean(dh xhat)
-    float4* out = reinterpret_cast<float4*>(dx + row * D);
+    float4* out = reinterpret_cast<float4*>(dx + (row0 + r) * D);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int i = threadIdx.x + k * AB_THREADS;
+      const int i = threadIdx.x + k * T;
       if (i < nv) {
-        const float4 sc = __ldg(scale + i);
-        const float4 r = __ldcs(rr + i);
-        const float2 g0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&g[k].x));
-        const float2 g1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&g[k].y));
+        const float4 g = unpack4(yr[i]), res = rr[i];
         const float4 xh = make_float4(v[k].x * rstd, v[k].y * rstd, v[k].z * rstd, v[k].w * rstd);
-        a_shift[k].x += g0.x;
-        a_shift[k].y += g0.y;
-        a_shift[k].z += g1.x;
-        a_shift[k].w += g1.y;
-        a_scale[k].x = fmaf(g0.x, xh.x, a_scale[k].x);
-        a_scale[k].y = fmaf(g0.y, xh.y, a_scale[k].y);
-        a_scale[k].z = fmaf(g1.x, xh.z, a_scale[k].z);
-        a_scale[k].w = fmaf(g1.y, xh.w, a_scale[k].w);
+        a_shift[k].x += g.x;
+        a_shift[k].y += g.y;
+        a_shift[k].z += g.z;
+        a_shift[k].w += g.w;
+        a_scale[k].x = fmaf(g.x, xh.x, a_scale[k].x);
+        a_scale[k].y = fmaf(g.y, xh.y, a_scale[k].y);
+        a_scale[k].z = fmaf(g.z, xh.z, a_scale[k].z);
+        a_scale[k].w = fmaf(g.w, xh.w, a_scale[k].w);
         float4 o;
-        o.x = fmaf(rstd, g0.x * (1.f + sc.x) - mean_h - xh.x * mean_hx, r.x);
-        o.y = fmaf(rstd, g0.y * (1.f + sc.y) - mean_h - xh.y * mean_hx, r.y);
-        o.z = fmaf(rstd, g1.x * (1.f + sc.z) - mean_h - xh.z * mean_hx, r.z);
-        o.w = fmaf(rstd, g1.y * (1.f + sc.w) - mean_h - xh.w * mean_hx, r.w);
+        o.x = fmaf(rstd, g.x * sc[k].x - mean_h - xh.x * mean_hx, res.x);
+        o.y = fmaf(rstd, g.y * sc[k].y - mean_h - xh.y * mean_hx, res.y);
+        o.z = fmaf(rstd, g.z * sc[k].z - mean_h - xh.z * mean_hx, res.z);
+        o.w = fmaf(rstd, g.w * sc[k].w - mean_h - xh.w * mean_hx, res.w);
         __stcs(out + i, o);
       }
     }
@@ -144,7 +188,7 @@ __global__ void __launch_bounds__(AB_THREADS) adaln_bwd_kernel(
   float4* p0 = reinterpret_cast<float4*>(part + (long)blockIdx.x * 2 * D);
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
-    const int i = threadIdx.x + k * AB_THREADS;
+    const int i = threadIdx.x + k * T;
     if (i < nv) {
       p0[i] = a_shift[k];
       p0[nv + i] = a_scale[k];
@@ -228,41 +272,43 @@ __global__ void __launch_bounds__(256) dv_rows_kernel(const bf16* __restrict__ d
 }  // namespace bwd_detail
 using namespace bwd_detail;
 
-// CTAs that the AdaLN backward pass spreads the valid rows over: two per SM.
-// Each modality's last one may be short, so up to two more partial rows.
-constexpr int ADALN_BWD_CTAS = 296;
-constexpr int ADALN_BWD_PARTS = ADALN_BWD_CTAS + 2;
+int adaln_bwd_parts(int D) { return adaln_plan(D).ctas; }
 
 cudaError_t launch_adaln_bwd(const float* x, const float* mod, int branch, const bf16* dy, const float* dres, float* dx,
                              const int* rstart, const int* rcount, int L, int L_pad, int D, float eps, float* part,
                              bf16* dmod, cudaStream_t stream) {
+  const AdalnPlan plan = adaln_plan(D);
   RangeArgs rg;
   Chunks ch;
-  const int per_cta = (L + ADALN_BWD_CTAS - 1) / ADALN_BWD_CTAS;
-  int n = 0;
+  // as few rows per CTA as let the three modalities' CTAs, whose last ones may
+  // be short, run in one wave
+  ch.rows = (L + plan.ctas - 1) / plan.ctas;
+  for (;; ++ch.rows) {
+    ch.first[0] = 0;
+    for (int m = 0; m < 3; ++m) ch.first[m + 1] = ch.first[m] + (rcount[m] + ch.rows - 1) / ch.rows;
+    if (ch.first[3] <= plan.ctas) break;
+  }
   for (int m = 0; m < 3; ++m) {
     rg.start[m] = rstart[m];
     rg.count[m] = rcount[m];
-    ch.first[m] = n;
-    ch.rows[m] = per_cta;
-    n += (rcount[m] + per_cta - 1) / per_cta;
   }
-  ch.first[3] = n;
-  const int pad = L_pad - L < ADALN_BWD_CTAS ? L_pad - L : ADALN_BWD_CTAS;
-  const int grid = n + pad;
+  const int pad = L_pad - L < plan.ctas ? L_pad - L : plan.ctas;
+  const int grid = ch.first[3] + pad, vpt = (D / 4 + plan.threads - 1) / plan.threads;
+  const int bytes = plan.stages * 10 * D;
+  static unsigned long long attr_done[4] = {0, 0, 0, 0};
 #define H3_ADALN_BWD(V)                                                                                              \
-  case V:                                                                                                            \
-    adaln_bwd_kernel<V><<<grid, AB_THREADS, 0, stream>>>(x, mod, branch, dy, dres, dx, rg, ch, L, L_pad, D, eps, part); \
-    break;
-  switch ((D + 1023) / 1024) {
+  case V: {                                                                                                          \
+    cudaError_t ea = ensure_smem_attr(reinterpret_cast<const void*>(adaln_bwd_kernel<V>), AB_SMEM, &attr_done[V - 1]); \
+    if (ea != cudaSuccess) return ea;                                                                                \
+    adaln_bwd_kernel<V><<<grid, plan.threads, bytes, stream>>>(x, mod, branch, dy, dres, dx, rg, ch, L, L_pad, D, eps, \
+                                                               plan.stages, part);                                   \
+    break;                                                                                                           \
+  }
+  switch (vpt) {
     H3_ADALN_BWD(1)
     H3_ADALN_BWD(2)
     H3_ADALN_BWD(3)
     H3_ADALN_BWD(4)
-    H3_ADALN_BWD(5)
-    H3_ADALN_BWD(6)
-    H3_ADALN_BWD(7)
-    H3_ADALN_BWD(8)
     default: return cudaErrorInvalidValue;
   }
 #undef H3_ADALN_BWD

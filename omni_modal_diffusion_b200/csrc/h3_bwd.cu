@@ -65,7 +65,7 @@ size_t h3_backward_workspace_bytes(const h3_dims* dims, int L_pad, int op) {
   if (!dims || L_pad <= 0 || dims->D <= 0 || dims->H <= 0 || dims->I <= 0 || dims->F <= 0) return 0;
   Carve c(nullptr);
   switch (op) {
-    case H3_BWD_ADALN: c.take<float>((size_t)ADALN_BWD_PARTS * 2 * dims->D); break;
+    case H3_BWD_ADALN: c.take<float>((size_t)adaln_bwd_parts(dims->D) * 2 * dims->D); break;
     case H3_BWD_QKV:
       c.take<bf16>((size_t)L_pad * 3 * dims->I);
       c.take<float>((size_t)QKNORM_PARTS * 2 * 128);

@@ -479,94 +479,112 @@ def h3_backward_workspace_bytes(dims, L_pad: int, op: int) -> int:
     return int(lib().h3_backward_workspace_bytes(ctypes.byref(dims), L_pad, op))
 
 
-def _call_backward(name, dims, ranges, op, tensors, stream, ints=()):
-    """One backward call: tensors is a list of (name, tensor, dtype, numel or
-    None, optional) in the order of the C arguments, ints {position: value} the
-    plain arguments among them.  Sizes are checked here, where they are known:
-    the C call sees only pointers.  The call runs on the tensors' device, on
-    `stream` or that device's current stream."""
-    dev = None
-    for n, t, dt, count, optional in tensors:
-        if t is None:
-            if optional:
-                continue
+def _call_backward(name, dims, ranges, stream, spec, tensors, counts, at=None, value=0):
+    """One backward call.  spec: (argument name, dtype, may be None) for each
+    tensor, in the order of the C arguments, `counts` their sizes in elements
+    (checked here, where they are known: the C call sees only pointers);
+    `value` is the plain argument at position `at`.  The call runs on the
+    tensors' device, on `stream` or that device's current stream."""
+    args, dev = [], -1
+    for (n, dt, optional), t, count in zip(spec, tensors, counts):
+        if t is None and optional:
+            args.append(None)
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{n} must be a CUDA tensor")
-        _ptr(t, dt, n)
-        if count is not None and t.numel() != count:
+        if t.dtype != dt:
+            raise TypeError(f"{n} must be {dt}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+        if n == "ws":
+            if t.numel() < count:
+                raise ValueError(f"workspace too small: {count} bytes needed")
+        elif t.numel() != count:
             raise ValueError(f"{n} must have {count} elements, got {t.numel()}")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{n} is on {t.device}, the others on {dev}")
-    if op is not None:
-        ws = tensors[-1][1]
-        need = h3_backward_workspace_bytes(dims, ranges.L_pad, op)
-        if ws.numel() * ws.element_size() < need:
-            raise ValueError(f"workspace too small: {need} bytes needed")
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-    args = [_ptr(t) for _, t, _, _, _ in tensors]
-    for at, v in sorted(dict(ints).items()):
-        args.insert(at, v)
-    with torch.cuda.device(dev):
-        _check(getattr(lib(), name)(ctypes.byref(dims), ctypes.byref(ranges), *args, _stream(stream)))
+        if dev < 0:
+            dev = t.get_device()
+        elif t.get_device() != dev:
+            raise ValueError(f"{n} is on device {t.get_device()}, the others on {dev}")
+        args.append(t.data_ptr())
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device_index != dev:
+        raise ValueError(f"the stream is on device {stream.device_index}, the tensors on {dev}")
+    if at is not None:
+        args.insert(at, value)
+    fn = getattr(_lib or lib(), name)
+    if torch.cuda.current_device() == dev:
+        rc = fn(dims, ranges, *args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(dims, ranges, *args, stream.cuda_stream)
+    if rc != H3_OK:
+        _check(rc)
+
+
+def _spec(*args):
+    return tuple((a[:-1], dt, True) if a.endswith("?") else (a, dt, False) for a, dt in args)
+
+
+_ADALN_BWD = _spec(("x", F32), ("mod", F32), ("dxm", BF16), ("dres", F32), ("dx", F32), ("dmod?", BF16), ("ws", U8))
+_QKV_BWD = _spec(("xm", BF16), ("Wqkv", BF16), ("qn_w", BF16), ("kn_w", BF16), ("pos", F32), ("dq", BF16), ("dk", BF16),
+                 ("dv", BF16), ("dxm", BF16), ("dWqkv?", BF16), ("dqn_w?", BF16), ("dkn_w?", BF16), ("ws", U8))
+_ATTENTION_LSE = _spec(("q", BF16), ("k", BF16), ("v", BF16), ("qn_w?", BF16), ("kn_w?", BF16), ("o", BF16), ("lse", F32))
+_ATTENTION_BWD = _spec(("q", BF16), ("k", BF16), ("v", BF16), ("o", BF16), ("lse", F32), ("do", BF16), ("dq", BF16),
+                       ("dk", BF16), ("dv", BF16), ("ws", U8))
+_GATED_BWD = _spec(("dx", F32), ("o", BF16), ("Wo", BF16), ("mod", F32), ("do", BF16), ("dWo?", BF16), ("dmod?", BF16),
+                   ("ws", U8))
+_FFN_BWD = _spec(("dx", F32), ("xm", BF16), ("Wgu", BF16), ("Wd", BF16), ("mod", F32), ("dxm", BF16), ("dWgu?", BF16),
+                 ("dWd?", BF16), ("dmod?", BF16), ("ws", U8))
 
 
 def h3_adaln_norm_modulate_backward(dims, ranges, x, mod, branch, dxm, dres, dx, dmod, ws, stream=None):
     """dx = dres + the gradient through the norm and modulation (dx may be
     dres); dmod [3][6][D] bf16 or None: the branch's shift and scale slots."""
-    n = ranges.L_pad * dims.D
-    _call_backward("h3_adaln_norm_modulate_backward", dims, ranges, H3_BWD_ADALN,
-                   [("x", x, F32, n, False), ("mod", mod, F32, 18 * dims.D, False), ("dxm", dxm, BF16, n, False),
-                    ("dres", dres, F32, n, False), ("dx", dx, F32, n, False), ("dmod", dmod, BF16, 18 * dims.D, True),
-                    ("ws", ws, U8, None, False)], stream, {2: branch})
+    n, m = ranges.L_pad * dims.D, 18 * dims.D
+    _call_backward("h3_adaln_norm_modulate_backward", dims, ranges, stream, _ADALN_BWD,
+                   (x, mod, dxm, dres, dx, dmod, ws),
+                   (n, m, n, n, n, m, h3_backward_workspace_bytes(dims, ranges.L_pad, H3_BWD_ADALN)), 2, branch)
 
 
 def h3_qkv_qknorm_mrope_backward(dims, ranges, xm, Wqkv, qn_w, kn_w, pos, dq, dk, dv, dxm, dWqkv, dqn_w, dkn_w, ws,
                                  stream=None):
     """dWqkv, dqn_w, dkn_w may be None (frozen weights)."""
     n, h, w = ranges.L_pad * dims.D, ranges.L_pad * dims.I, 3 * dims.I * dims.D
-    _call_backward("h3_qkv_qknorm_mrope_backward", dims, ranges, H3_BWD_QKV,
-                   [("xm", xm, BF16, n, False), ("Wqkv", Wqkv, BF16, w, False), ("qn_w", qn_w, BF16, 128, False),
-                    ("kn_w", kn_w, BF16, 128, False), ("pos", pos, F32, ranges.L_pad * 3, False),
-                    ("dq", dq, BF16, h, False), ("dk", dk, BF16, h, False), ("dv", dv, BF16, h, False),
-                    ("dxm", dxm, BF16, n, False), ("dWqkv", dWqkv, BF16, w, True), ("dqn_w", dqn_w, BF16, 128, True),
-                    ("dkn_w", dkn_w, BF16, 128, True), ("ws", ws, U8, None, False)], stream)
+    _call_backward("h3_qkv_qknorm_mrope_backward", dims, ranges, stream, _QKV_BWD,
+                   (xm, Wqkv, qn_w, kn_w, pos, dq, dk, dv, dxm, dWqkv, dqn_w, dkn_w, ws),
+                   (n, w, 128, 128, ranges.L_pad * 3, h, h, h, n, w, 128, 128,
+                    h3_backward_workspace_bytes(dims, ranges.L_pad, H3_BWD_QKV)))
 
 
 def h3_attention_lse(dims, ranges, q, k, v, o, lse, qn_w=None, kn_w=None, stream=None):
     """h3_attention on normalised and rotated q, k, which also writes each
     row's log-sum-exp, lse [H][L_pad] fp32."""
     h = ranges.L_pad * dims.I
-    _call_backward("h3_attention_lse", dims, ranges, None,
-                   [("q", q, BF16, h, False), ("k", k, BF16, h, False), ("v", v, BF16, h, False),
-                    ("qn_w", qn_w, BF16, 128, True), ("kn_w", kn_w, BF16, 128, True), ("o", o, BF16, h, False),
-                    ("lse", lse, F32, dims.H * ranges.L_pad, False)], stream)
+    _call_backward("h3_attention_lse", dims, ranges, stream, _ATTENTION_LSE, (q, k, v, qn_w, kn_w, o, lse),
+                   (h, h, h, 128, 128, h, dims.H * ranges.L_pad))
 
 
 def h3_attention_backward(dims, ranges, q, k, v, o, lse, do, dq, dk, dv, ws, stream=None):
     h = ranges.L_pad * dims.I
-    _call_backward("h3_attention_backward", dims, ranges, H3_BWD_ATTENTION,
-                   [(n, t, BF16, h, False) for n, t in (("q", q), ("k", k), ("v", v), ("o", o))]
-                   + [("lse", lse, F32, dims.H * ranges.L_pad, False)]
-                   + [(n, t, BF16, h, False) for n, t in (("do", do), ("dq", dq), ("dk", dk), ("dv", dv))]
-                   + [("ws", ws, U8, None, False)], stream)
+    _call_backward("h3_attention_backward", dims, ranges, stream, _ATTENTION_BWD,
+                   (q, k, v, o, lse, do, dq, dk, dv, ws),
+                   (h, h, h, h, dims.H * ranges.L_pad, h, h, h, h,
+                    h3_backward_workspace_bytes(dims, ranges.L_pad, H3_BWD_ATTENTION)))
 
 
 def h3_gated_residual_backward(dims, ranges, dx, o, Wo, mod, do, dWo, dmod, ws, branch=H3_MSA, stream=None):
     """dWo, dmod may be None; dmod: the branch's gate slot."""
-    h, w = ranges.L_pad * dims.I, dims.D * dims.I
-    _call_backward("h3_gated_residual_backward", dims, ranges, H3_BWD_GATED_RESIDUAL,
-                   [("dx", dx, F32, ranges.L_pad * dims.D, False), ("o", o, BF16, h, False), ("Wo", Wo, BF16, w, False),
-                    ("mod", mod, F32, 18 * dims.D, False), ("do", do, BF16, h, False), ("dWo", dWo, BF16, w, True),
-                    ("dmod", dmod, BF16, 18 * dims.D, True), ("ws", ws, U8, None, False)], stream, {4: branch})
+    h, w, m = ranges.L_pad * dims.I, dims.D * dims.I, 18 * dims.D
+    _call_backward("h3_gated_residual_backward", dims, ranges, stream, _GATED_BWD,
+                   (dx, o, Wo, mod, do, dWo, dmod, ws),
+                   (ranges.L_pad * dims.D, h, w, m, h, w, m,
+                    h3_backward_workspace_bytes(dims, ranges.L_pad, H3_BWD_GATED_RESIDUAL)), 4, branch)
 
 
 def h3_ffn_swiglu_backward(dims, ranges, dx, xm, Wgu, Wd, mod, dxm, dWgu, dWd, dmod, ws, stream=None):
     """dWgu, dWd, dmod may be None; dmod: the gate_mlp slot."""
-    n, w = ranges.L_pad * dims.D, dims.D * dims.F
-    _call_backward("h3_ffn_swiglu_backward", dims, ranges, H3_BWD_FFN,
-                   [("dx", dx, F32, n, False), ("xm", xm, BF16, n, False), ("Wgu", Wgu, BF16, 2 * w, False),
-                    ("Wd", Wd, BF16, w, False), ("mod", mod, F32, 18 * dims.D, False), ("dxm", dxm, BF16, n, False),
-                    ("dWgu", dWgu, BF16, 2 * w, True), ("dWd", dWd, BF16, w, True),
-                    ("dmod", dmod, BF16, 18 * dims.D, True), ("ws", ws, U8, None, False)], stream)
+    n, w, m = ranges.L_pad * dims.D, dims.D * dims.F, 18 * dims.D
+    _call_backward("h3_ffn_swiglu_backward", dims, ranges, stream, _FFN_BWD,
+                   (dx, xm, Wgu, Wd, mod, dxm, dWgu, dWd, dmod, ws),
+                   (n, n, 2 * w, w, m, n, 2 * w, w, m, h3_backward_workspace_bytes(dims, ranges.L_pad, H3_BWD_FFN)))
