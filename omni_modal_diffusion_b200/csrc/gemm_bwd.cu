@@ -34,6 +34,7 @@ enum Kind : int { DGRAD = 0, WGRAD = 1, GATED = 2, QKNORM = 3, FFN = 4 };
 
 struct Maps {
   CUtensorMap a[3], b[3];  // per segment (GATED), else index 0; FFN: a[1], b[1] are dY and Wd
+  CUtensorMap w;           // GATED: W, 128-row boxes
 };
 
 struct Params {
@@ -46,8 +47,8 @@ struct Params {
   // GATED
   const float* mod;   // [3][6][D]
   int gate_slot, D;
-  const bf16* W;      // [M][N], the weight behind the gate (null: no gate gradient)
-  float* gate_part;   // [3][2 n_tiles][M] column-tile partials of the gate's gradient
+  int gate_grad;      // whether the gate's gradient is wanted
+  float* gate_part;   // [3][4 n_tiles][M] column-quarter partials of the gate's gradient
   // FFN
   bf16* h;            // [.][F]
   bf16* dgu;          // [.][2F]
@@ -65,28 +66,64 @@ struct Params {
 
 constexpr int BK = 64;
 constexpr int OPERAND = 128 * BK * 2;  // one 128 x 64 operand tile of a CTA, 16 KB
-constexpr int THREADS = 320;           // warp 0 TMA, warp 1 MMA, warps 2-9 epilogue
 template <int KIND>
 struct Cfg {
   static constexpr bool FFN_ = KIND == FFN;
-  static constexpr int STAGES = FFN_ ? 4 : 6;
+  static constexpr int STAGES = FFN_ || KIND == GATED ? 4 : 6;
   // FFN: xm, dY (16 KB each), gate or up rows of Wgu (16 KB), 64 columns of Wd (8 KB)
   static constexpr int STAGE = FFN_ ? 3 * OPERAND + OPERAND / 2 : 2 * OPERAND;
   static constexpr int ACCS = FFN_ ? 1 : 2;  // TMEM accumulators: 256 + 128 columns, or 2 x 256
+  // Warp 0 TMA, warp 1 MMA, then EW epilogue warps: EW / 4 of each TMEM lane
+  // quarter, sharing the tile's columns.  Sixteen hide the latency of the
+  // TMEM and global accesses of one tile; QKNORM needs a head's 128 columns in
+  // one warp and has eight.
+  static constexpr int EW = KIND == QKNORM ? 8 : 16;
+  // GATED: one more warp loads the tile of W that the gate's gradient needs
+  static constexpr int THREADS = (2 + EW + (KIND == GATED ? 1 : 0)) * 32;
+  static constexpr int WTILE = KIND == GATED ? 4 * OPERAND : 0;  // 128 rows x 256 columns
   static constexpr int MISC = 768;
   static constexpr int NORM = KIND == QKNORM ? 8 * 2 * 128 * 4 : 0;  // [epilogue warp][q, k][128]
-  static constexpr int BYTES = STAGES * STAGE + 1024 + MISC + NORM;
+  static constexpr int BYTES = STAGES * STAGE + WTILE + 1024 + MISC + NORM;
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
 
 __device__ __forceinline__ void ld_chunk(uint32_t taddr, float* v) {
   tmem_ld32(taddr, reinterpret_cast<uint32_t*>(v));
 }
-__device__ __forceinline__ void store32(bf16* dst, const float* v) {
+// 32 lanes x 16 consecutive 32-bit columns
+__device__ __forceinline__ void ld_chunk16(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void st_v4(bf16* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// 16 columns of row m (lane = m % 32) as 8 words of bf16 pairs.  Lanes 2i and
+// 2i + 1 exchange halves so that each store instruction writes whole 32-byte
+// sectors: first the even rows', then the odd rows'.  Warp-collective.
+__device__ __forceinline__ void store16(bf16* dst, long ld, int m, int M, const uint32_t* w) {
+  const bool odd = (threadIdx.x & 1) != 0;
+  uint32_t t[4], e[4], o[4];
 #pragma unroll
-  for (int j = 0; j < 32; j += 8)
-    *reinterpret_cast<uint4*>(dst + j) = make_uint4(pack_bf16x2(v[j], v[j + 1]), pack_bf16x2(v[j + 2], v[j + 3]),
-                                                    pack_bf16x2(v[j + 4], v[j + 5]), pack_bf16x2(v[j + 6], v[j + 7]));
+  for (int i = 0; i < 4; ++i) {
+    t[i] = __shfl_xor_sync(0xffffffffu, odd ? w[i] : w[4 + i], 1);
+    e[i] = odd ? t[i] : w[i];
+    o[i] = odd ? w[4 + i] : t[i];
+  }
+  // the lane's place in the even and in the odd row of its pair
+  bf16* pe = dst + (odd ? 8 - ld : 0L);
+  bf16* po = dst + (odd ? 8L : ld);
+  if ((m & ~1) < M) st_v4(pe, e[0], e[1], e[2], e[3]);
+  if ((m | 1) < M) st_v4(po, o[0], o[1], o[2], o[3]);
+}
+template <int N>
+__device__ __forceinline__ void pack_row(const float* v, uint32_t* w) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) w[i / 2] = pack_bf16x2(v[i], v[i + 1]);
 }
 __device__ __forceinline__ void unpack8(const uint4& u, float* f) {
   const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&u);
@@ -126,10 +163,10 @@ __device__ __forceinline__ void unrotate32(const bf16* d, bool valid, const floa
 // dx = inv (dh - xhat mean(dh xhat)); with s = sum dh x, mean(dh xhat) =
 // s inv / 128.  Two passes over the row's four chunks; sum_t t xhat, the
 // gradient of w, goes to wacc[128] of this warp.
+template <typename Release>
 __device__ __forceinline__ void epi_qknorm(const Params& p, uint32_t tb, int m, int n, const float* freq,
-                                           const uint8_t* axis, float* wacc2) {
+                                           const uint8_t* axis, float* wacc2, Release release) {
   const int lane = threadIdx.x & 31;
-  if (n >= p.N) return;  // uniform
   const int part = n / p.I, hd = (n % p.I) / 128;
   const bool valid = m < p.rows;
   const bf16* d = (part == 0 ? p.dq : p.dk) + ((long)hd * p.L_pad + (valid ? m : 0)) * 128;
@@ -161,8 +198,8 @@ __device__ __forceinline__ void epi_qknorm(const Params& p, uint32_t tb, int m, 
   }
   const float inv = rsqrtf(ss * (1.0f / 128.0f) + p.eps_qk);
   const float mean = s * inv * (1.0f / 128.0f);
-  bf16* dst = p.out + (long)m * p.ldo + n;
-#pragma unroll 1
+  uint32_t out[64];
+#pragma unroll
   for (int c = 0; c < 4; ++c) {
     float x[32], t[32];
     ld_chunk(tb + c * 32, x);
@@ -179,7 +216,7 @@ __device__ __forceinline__ void epi_qknorm(const Params& p, uint32_t tb, int m, 
         t[j + i] *= xh;
       }
     }
-    if (valid) store32(dst + c * 32, x);
+    pack_row<32>(x, out + c * 16);
     // sum over the warp's 32 rows: lane l ends with column l of the chunk
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -192,58 +229,74 @@ __device__ __forceinline__ void epi_qknorm(const Params& p, uint32_t tb, int m, 
     }
     wacc[c * 32 + lane] += t[0];
   }
+  release();
+  bf16* dst = p.out + (long)m * p.ldo + n;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) store16(dst + c * 16, p.ldo, m, p.rows, out + c * 8);
 }
 
-// h = SiLU(g) u, du = dh SiLU(g), dg = dh u sig(g) (1 + g (1 - sig(g))) for this
-// warp's 64 of the tile's 128 hidden columns; accumulator columns [0, 128) g,
-// [128, 256) u, [256, 384) dh
-__device__ __forceinline__ void epi_ffn(const Params& p, uint32_t tb, int m, int nt, int sub) {
-  bf16* hrow = p.h + (long)m * p.F + (long)nt * 128;
-  bf16* grow = p.dgu + (long)m * 2 * p.F + (long)nt * 128;
-#pragma unroll 1
-  for (int c = sub * 2; c < sub * 2 + 2; ++c) {
-    float g[32], u[32], dh[32];
-    ld_chunk(tb + c * 32, g);
-    ld_chunk(tb + 128 + c * 32, u);
-    ld_chunk(tb + 256 + c * 32, dh);
+// h = SiLU(g) u, du = dh SiLU(g), dg = dh u sig(g) (1 + g (1 - sig(g))) for 32 of
+// the tile's 128 hidden columns; accumulator columns [0, 128) g, [128, 256) u,
+// [256, 384) dh
+template <typename Release>
+__device__ __forceinline__ void epi_ffn(const Params& p, uint32_t tb, int m, int nt, int sub, Release release) {
+  uint32_t hw[16], gw[16], uw[16];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    float g[16], u[16], dh[16];
+    const uint32_t t0 = tb + sub * 32 + c * 16;
+    ld_chunk16(t0, g);
+    ld_chunk16(t0 + 128, u);
+    ld_chunk16(t0 + 256, dh);
     tmem_wait_ld();
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
+    for (int j = 0; j < 16; ++j) {
       const float sig = __fdividef(1.0f, 1.0f + __expf(-g[j]));
       const float act = g[j] * sig;
       const float dact = sig + act * (1.0f - sig);
       const float d = dh[j];
-      dh[j] = act * u[j];          // h
-      g[j] = d * u[j] * dact;      // dg
-      u[j] = d * act;              // du
+      dh[j] = act * u[j];      // h
+      g[j] = d * u[j] * dact;  // dg
+      u[j] = d * act;          // du
     }
-    if (m < p.rows) {
-      store32(hrow + c * 32, dh);
-      store32(grow + c * 32, g);
-      store32(grow + p.F + c * 32, u);
-    }
+    pack_row<16>(dh, hw + c * 8);
+    pack_row<16>(g, gw + c * 8);
+    pack_row<16>(u, uw + c * 8);
+  }
+  release();
+  bf16* hrow = p.h + (long)m * p.F + (long)nt * 128 + sub * 32;
+  bf16* grow = p.dgu + (long)m * 2 * p.F + (long)nt * 128 + sub * 32;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    store16(hrow + c * 16, p.F, m, p.rows, hw + c * 8);
+    store16(grow + c * 16, 2L * p.F, m, p.rows, gw + c * 8);
+    store16(grow + p.F + c * 16, 2L * p.F, m, p.rows, uw + c * 8);
   }
 }
 
 template <int KIND>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 1)
     gemm_bwd_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   using C = Cfg<KIND>;
-  constexpr int STAGES = C::STAGES, STAGE = C::STAGE;
+  constexpr int STAGES = C::STAGES, STAGE = C::STAGE, EW = C::EW;
+  constexpr int COLS = 1024 / EW;  // output columns of an epilogue warp (FFN: 32)
   constexpr bool A_MN = KIND == WGRAD || KIND == GATED;
   constexpr bool B_MN = KIND != QKNORM && KIND != FFN;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE);
+  uint8_t* sW = smem + STAGES * STAGE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE + C::WTILE);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* w_full = drain + 1;   // GATED: W of the tile
+  uint64_t* w_empty = drain + 2;  // GATED: read by every epilogue warp of this CTA
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 3);
   float* freq = reinterpret_cast<float*>(tmem_slot + 4);
   uint8_t* axis = reinterpret_cast<uint8_t*>(freq + 64);
-  float* wacc = reinterpret_cast<float*>(smem + STAGES * STAGE + C::MISC);
+  float* wacc = reinterpret_cast<float*>(smem + STAGES * STAGE + C::WTILE + C::MISC);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = cluster_ctarank();
@@ -257,9 +310,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);    // the leader's commit, delivered to both CTAs
-      mbar_init(&tempty[a], 16);  // 8 epilogue warps in each CTA (leader's copy used)
+      mbar_init(&tempty[a], 2 * EW);  // the epilogue warps of both CTAs (leader's copy used)
     }
     mbar_init(drain, 1);
+    mbar_init(w_full, 1);
+    mbar_init(w_empty, EW);
     fence_mbar_init();
     tma_prefetch_desc(&maps.a[0]);
     tma_prefetch_desc(&maps.b[0]);
@@ -279,7 +334,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       freq[i] = powf(p.theta, -2.0f * (float)i_sec / (float)d_sec);
       axis[i] = (uint8_t)ax;
     }
-    for (int i = threadIdx.x; i < 8 * 2 * 128; i += THREADS) wacc[i] = 0.f;
+    for (int i = threadIdx.x; i < 8 * 2 * 128; i += C::THREADS) wacc[i] = 0.f;
   }
   tc_fence_before();
   __syncthreads();
@@ -385,9 +440,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       umma_commit_pair(drain);
       mbar_wait(drain, 0);
     }
+  } else if (warp >= 2 + EW) {  // GATED: the tiles of W
+    if (lane == 0 && p.gate_grad) {
+      int n = 0;
+      for (int t = pair; t < num_tiles; t += n_pairs, ++n) {
+        int mt, nt;
+        tile_coords(t, p.m_tiles, p.n_tiles, p.group_m, mt, nt);
+        if (!mbar_wait(w_empty, (n & 1) ^ 1)) break;
+        mbar_arrive_expect_tx(w_full, C::WTILE);
+        for (int c = 0; c < 4; ++c)
+          tma_load_2d(sW + c * OPERAND, &maps.w, w_full, nt * 256 + c * 64, mt * 256 + (int)rank * 128);
+      }
+      if (n > 0) mbar_wait(w_full, (n - 1) & 1);
+    }
   } else {
     const int q = warp & 3;           // TMEM lane quarter
-    const int sub = (warp - 2) >> 2;  // which half of the tile's columns
+    const int sub = (warp - 2) >> 2;  // which share of the tile's columns
     const int row_in_tile = q * 32 + lane;
     const uint32_t tempty_leader = mapa_shared(smem_u32(&tempty[0]), 0);
     int acc = 0;
@@ -405,70 +473,90 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (++acc == C::ACCS) { acc = 0; acc_phase ^= 1; }
     };
     const uint32_t lane_off = (uint32_t)(q * 32) << 16;
+    int n_tile = 0;
     for (int t = pair; t < num_tiles; t += n_pairs) {
       int mt, nt;
       tile_coords(t, p.m_tiles, p.n_tiles, p.group_m, mt, nt);
       const int m = mt * 256 + (int)rank * 128 + row_in_tile;
-      const int n0 = nt * 256 + sub * 128;
+      const int n0 = nt * 256 + sub * COLS;
       if constexpr (KIND == GATED) {
-        // the tile's 128 output columns of this row stay in registers while
-        // the modalities' accumulators come by
-        float sum[128];
+        // the warp's 64 output columns of this row stay in registers while the
+        // modalities' accumulators come by; W's 64 columns (one swizzled box)
+        // are in shared memory
+        float sum[COLS];
 #pragma unroll
-        for (int j = 0; j < 128; ++j) sum[j] = 0.f;
+        for (int j = 0; j < COLS; ++j) sum[j] = 0.f;
         const bool in = m < p.M;
-        for (int sg = 0; sg < 3 && ok; ++sg) {
+        const uint8_t* wrow = sW + sub * OPERAND + row_in_tile * 128;
+        if (p.gate_grad) {
+          ok = mbar_wait_warp(w_full, n_tile & 1);
+          if (!ok) break;
+        }
+#pragma unroll 1
+        for (int sg = 0; sg < 3; ++sg) {
           if (p.seg_rows[sg] == 0) continue;
-          if (!wait_full()) break;
-          const uint32_t tb = tmem_base + lane_off + (uint32_t)(acc * 256 + sub * 128);
           const float gate = in ? __ldg(p.mod + (long)(sg * 6 + p.gate_slot) * p.D + m) : 0.f;
+          if (!wait_full()) break;
+          const uint32_t tb = tmem_base + lane_off + (uint32_t)(acc * 256 + sub * COLS);
           float dot = 0.f;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float v[32];
-            ld_chunk(tb + c * 32, v);
+          for (int c = 0; c < COLS; c += 16) {
+            float v[16];
+            ld_chunk16(tb + c, v);
             tmem_wait_ld();
-            const bool wanted = p.W != nullptr && in && n0 + c * 32 < p.N;
+            if (p.gate_grad) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              float wv[8];
-              unpack8(wanted ? __ldg(reinterpret_cast<const uint4*>(p.W + (long)m * p.N + n0 + c * 32 + j))
-                             : make_uint4(0, 0, 0, 0), wv);
+              for (int j = 0; j < 16; j += 8) {
+                float wv[8];
+                unpack8(*reinterpret_cast<const uint4*>(wrow + ((((c + j) >> 3) ^ (row_in_tile & 7)) << 4)), wv);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                dot = fmaf(wv[i], v[j + i], dot);
-                sum[c * 32 + j + i] = fmaf(gate, v[j + i], sum[c * 32 + j + i]);
+                for (int i = 0; i < 8; ++i) dot = fmaf(wv[i], v[j + i], dot);
               }
             }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[c + j] = fmaf(gate, v[j], sum[c + j]);
           }
           release();
-          if (p.W != nullptr && in) p.gate_part[((long)sg * 2 * p.n_tiles + nt * 2 + sub) * p.M + m] = dot;
+          if (p.gate_grad && in) p.gate_part[((long)sg * 4 * p.n_tiles + nt * 4 + sub) * p.M + m] = dot;
         }
         if (!ok) break;
-        if (p.out != nullptr && in) {
+        if (p.gate_grad) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(w_empty);
+        }
+        if (p.out != nullptr) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (n0 + c * 32 < p.N) store32(p.out + (long)m * p.ldo + n0 + c * 32, sum + c * 32);
+          for (int c = 0; c < COLS; c += 16) {
+            uint32_t w[8];
+            pack_row<16>(sum + c, w);
+            if (n0 + c < p.N) store16(p.out + (long)m * p.ldo + n0 + c, p.ldo, m, p.M, w);
+          }
         }
       } else {
         if (!wait_full()) break;
         const uint32_t tb = tmem_base + lane_off + (uint32_t)(acc * 256);
+        // the accumulator is handed back before the tile's stores: the release
+        // at cluster scope waits for every store before it
         if constexpr (KIND == FFN) {
-          epi_ffn(p, tb, m, nt, sub);
+          epi_ffn(p, tb, m, nt, sub, release);
         } else if constexpr (KIND == QKNORM) {
-          epi_qknorm(p, tb + sub * 128, m, n0, freq, axis, wacc + (warp - 2) * 256);
+          epi_qknorm(p, tb + sub * COLS, m, n0, freq, axis, wacc + (warp - 2) * 256, release);
         } else {
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            if (n0 + c * 32 >= p.N) break;
+          uint32_t w[COLS / 2];
+#pragma unroll
+          for (int c = 0; c < COLS; c += 32) {
             float v[32];
-            ld_chunk(tb + sub * 128 + c * 32, v);
+            ld_chunk(tb + sub * COLS + c, v);
             tmem_wait_ld();
-            if (m < p.M) store32(p.out + (long)m * p.ldo + n0 + c * 32, v);
+            pack_row<32>(v, w + c / 2);
           }
+          release();
+#pragma unroll
+          for (int c = 0; c < COLS; c += 16)
+            if (n0 + c < p.N) store16(p.out + (long)m * p.ldo + n0 + c, p.ldo, m, p.M, w + c / 2);
         }
-        release();
       }
+      ++n_tile;
     }
   }
 
@@ -508,7 +596,7 @@ cudaError_t launch(const Maps& maps, Params p, cudaStream_t stream) {
   const int tiles = p.m_tiles * p.n_tiles;
   const int max_pairs = max_cta_pairs();
   const int pairs = tiles < max_pairs ? tiles : max_pairs;
-  gemm_bwd_kernel<KIND><<<2 * pairs, THREADS, Cfg<KIND>::BYTES, stream>>>(maps, p);
+  gemm_bwd_kernel<KIND><<<2 * pairs, Cfg<KIND>::THREADS, Cfg<KIND>::BYTES, stream>>>(maps, p);
   return cudaGetLastError();
 }
 
@@ -556,11 +644,11 @@ cudaError_t launch_wgrad(const bf16* A, const bf16* B, int rows, int M, int N, b
   return launch<WGRAD>(maps, p, stream);
 }
 
-int gate_parts(int N) { return 2 * ((N + 255) / 256); }
+int gate_parts(int N) { return 4 * ((N + 255) / 256); }
 
 // dW [M][N] = sum_m gate_m (.) A_m^T B_m over the modality ranges, and the
 // column-tile partials of the gate's gradient into part [3][gate_parts(N)][M]
-// (W == nullptr: none; out == nullptr: no weight gradient)
+// (W, the weight behind the gate: null: none; out == nullptr: no weight gradient)
 cudaError_t launch_wgrad_gated(const bf16* A, const bf16* B, const int* start, const int* count, int M, int N,
                                const float* mod, int gate_slot, const bf16* W, bf16* out, float* part,
                                cudaStream_t stream) {
@@ -583,7 +671,8 @@ cudaError_t launch_wgrad_gated(const bf16* A, const bf16* B, const int* start, c
   p.mod = mod;
   p.gate_slot = gate_slot;
   p.D = M;
-  p.W = W;
+  p.gate_grad = W != nullptr;
+  if (W != nullptr && !map_k(&maps.w, W, M, N, N)) return cudaErrorInvalidValue;
   p.gate_part = part;
   return launch<GATED>(maps, p, stream);
 }
