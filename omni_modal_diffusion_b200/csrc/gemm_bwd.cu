@@ -40,6 +40,10 @@ struct Maps {
 struct Params {
   int M, N, K;  // output rows and columns; contraction length (unused by WGRAD, GATED)
   int m_tiles, n_tiles, group_m;
+  // The contraction in `splits` equal runs of k blocks, each a unit of work of
+  // its own that writes an fp32 partial, part [splits][M][N]; 1: none
+  int splits;
+  float* part;
   int rows;           // valid token rows
   int seg_rows[3];    // WGRAD: [0] = rows; GATED: tokens of each modality
   bf16* out;          // DGRAD, WGRAD, GATED (may be null): [M][ldo]
@@ -48,7 +52,7 @@ struct Params {
   const float* mod;   // [3][6][D]
   int gate_slot, D;
   int gate_grad;      // whether the gate's gradient is wanted
-  float* gate_part;   // [3][4 n_tiles][M] column-quarter partials of the gate's gradient
+  float* gate_part;   // [3][splits * 4 n_tiles][M] column-quarter partials of the gate's gradient
   // FFN
   bf16* h;            // [.][F]
   bf16* dgu;          // [.][2F]
@@ -99,13 +103,14 @@ __device__ __forceinline__ void ld_chunk16(uint32_t taddr, float* v) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void st_v4(bf16* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+__device__ __forceinline__ void st_v4(uint32_t* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-// 16 columns of row m (lane = m % 32) as 8 words of bf16 pairs.  Lanes 2i and
-// 2i + 1 exchange halves so that each store instruction writes whole 32-byte
-// sectors: first the even rows', then the odd rows'.  Warp-collective.
-__device__ __forceinline__ void store16(bf16* dst, long ld, int m, int M, const uint32_t* w) {
+// 8 words of row m (lane = m % 32): 16 bf16 or 8 fp32 columns; ld in words.
+// Lanes 2i and 2i + 1 exchange halves so that each store instruction writes
+// whole 32-byte sectors: first the even rows', then the odd rows'.
+// Warp-collective.
+__device__ __forceinline__ void store8w(uint32_t* dst, long ld, int m, int M, const uint32_t* w) {
   const bool odd = (threadIdx.x & 1) != 0;
   uint32_t t[4], e[4], o[4];
 #pragma unroll
@@ -115,10 +120,21 @@ __device__ __forceinline__ void store16(bf16* dst, long ld, int m, int M, const 
     o[i] = odd ? w[4 + i] : t[i];
   }
   // the lane's place in the even and in the odd row of its pair
-  bf16* pe = dst + (odd ? 8 - ld : 0L);
-  bf16* po = dst + (odd ? 8L : ld);
+  uint32_t* pe = dst + (odd ? 4 - ld : 0L);
+  uint32_t* po = dst + (odd ? 4L : ld);
   if ((m & ~1) < M) st_v4(pe, e[0], e[1], e[2], e[3]);
   if ((m | 1) < M) st_v4(po, o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ void store16(bf16* dst, long ld, int m, int M, const uint32_t* w) {
+  store8w(reinterpret_cast<uint32_t*>(dst), ld / 2, m, M, w);
+}
+// the warp's columns [n0, n0 + COLS) of one split's fp32 partial [M][N]
+template <int COLS>
+__device__ __forceinline__ void store_part(float* part, int N, int n0, int m, int M, const float* v) {
+#pragma unroll
+  for (int c = 0; c < COLS; c += 8)
+    if (n0 + c < N)
+      store8w(reinterpret_cast<uint32_t*>(part + (long)m * N + n0 + c), N, m, M, reinterpret_cast<const uint32_t*>(v + c));
 }
 template <int N>
 __device__ __forceinline__ void pack_row(const float* v, uint32_t* w) {
@@ -343,9 +359,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
   const uint32_t tmem_base = *tmem_slot;
 
   const int num_tiles = p.m_tiles * p.n_tiles;
+  const int num_units = num_tiles * p.splits;
   constexpr int SEGS = KIND == GATED ? 3 : 1;
   auto seg_kb = [&](int sg) {
     return (KIND == WGRAD || KIND == GATED) ? (p.seg_rows[sg] + BK - 1) / BK : p.K / BK;
+  };
+  int kb_total = 0;
+  for (int sg = 0; sg < SEGS; ++sg) kb_total += seg_kb(sg);
+  const int kb_split = (kb_total + p.splits - 1) / p.splits;
+  // k blocks [lo, hi) of segment sg in split sp, the segments' blocks counted
+  // one after another
+  auto seg_range = [&](int sp, int sg, int& lo, int& hi) {
+    int before = 0;
+    for (int i = 0; i < sg; ++i) before += seg_kb(i);
+    const int n = seg_kb(sg);
+    lo = min(n, max(0, sp * kb_split - before));
+    hi = max(lo, min(n, (sp + 1) * kb_split - before));
   };
 
   if (warp == 0) {
@@ -355,14 +384,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       uint32_t phase = 0;
       long long issued = 0;
       bool ok = true;
-      for (int t = pair; t < num_tiles && ok; t += n_pairs) {
+      for (int u = pair; u < num_units && ok; u += n_pairs) {
         int mt, nt;
-        tile_coords(t, p.m_tiles, p.n_tiles, p.group_m, mt, nt);
+        const int sp = u / num_tiles;
+        tile_coords(u - sp * num_tiles, p.m_tiles, p.n_tiles, p.group_m, mt, nt);
         const int a0 = mt * 256 + (int)rank * 128;  // this CTA's A rows (or MN-major columns)
         const int b0 = nt * (KIND == FFN ? 128 : 256) + (int)rank * (KIND == FFN ? p.F : 128);
         for (int sg = 0; sg < SEGS && ok; ++sg) {
-          const int num_kb = seg_kb(sg);
-          for (int kb = 0; kb < num_kb; ++kb) {
+          int lo, hi;
+          seg_range(sp, sg, lo, hi);
+          for (int kb = lo; kb < hi; ++kb) {
             if (!mbar_wait(&empty[stage], phase ^ 1)) { ok = false; break; }
             if (leader) mbar_arrive_expect_tx(&full[stage], 2 * STAGE);
             const uint32_t fb = leader_full0 + stage * 8;
@@ -409,26 +440,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
-      for (int t = pair; t < num_tiles && ok; t += n_pairs) {
+      for (int u = pair; u < num_units && ok; u += n_pairs) {
         for (int sg = 0; sg < SEGS && ok; ++sg) {
-          const int num_kb = seg_kb(sg);
-          if (num_kb == 0) continue;
+          int lo, hi;
+          seg_range(u / num_tiles, sg, lo, hi);
+          if (lo == hi) continue;
           if (!mbar_wait_warp(&tempty[acc], acc_phase ^ 1)) { ok = false; break; }
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + (uint32_t)(acc * 256);
-          for (int kb = 0; kb < num_kb; ++kb) {
+          for (int kb = lo; kb < hi; ++kb) {
             if (!mbar_wait_warp(&full[stage], phase)) { ok = false; break; }
             tc_fence_after();
             const uint64_t off = (uint64_t)((stage * STAGE) >> 4);
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
               umma_bf16_pair(d_tmem, a_desc0 + off + kk * A_STEP, b_desc0 + off + kk * B_STEP, idesc,
-                             (kb | kk) != 0 ? 1u : 0u);
+                             (kb != lo || kk != 0) ? 1u : 0u);
             if constexpr (KIND == FFN) {
 #pragma unroll
               for (int kk = 0; kk < BK / 16; ++kk)
                 umma_bf16_pair(d_tmem + 256, a2_desc0 + off + kk * 2, b2_desc0 + off + kk * 128, idesc_dh,
-                               (kb | kk) != 0 ? 1u : 0u);
+                               (kb != lo || kk != 0) ? 1u : 0u);
             }
             umma_commit_pair(&empty[stage]);
             if (++stage == STAGES) { stage = 0; phase ^= 1; }
@@ -443,9 +475,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
   } else if (warp >= 2 + EW) {  // GATED: the tiles of W
     if (lane == 0 && p.gate_grad) {
       int n = 0;
-      for (int t = pair; t < num_tiles; t += n_pairs, ++n) {
+      for (int u = pair; u < num_units; u += n_pairs, ++n) {
         int mt, nt;
-        tile_coords(t, p.m_tiles, p.n_tiles, p.group_m, mt, nt);
+        tile_coords(u % num_tiles, p.m_tiles, p.n_tiles, p.group_m, mt, nt);
         if (!mbar_wait(w_empty, (n & 1) ^ 1)) break;
         mbar_arrive_expect_tx(w_full, C::WTILE);
         for (int c = 0; c < 4; ++c)
@@ -469,14 +501,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
     auto release = [&]() {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(tempty_leader + acc * 8);
+      if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + acc * 8);
       if (++acc == C::ACCS) { acc = 0; acc_phase ^= 1; }
     };
     const uint32_t lane_off = (uint32_t)(q * 32) << 16;
     int n_tile = 0;
-    for (int t = pair; t < num_tiles; t += n_pairs) {
+    for (int u = pair; u < num_units; u += n_pairs) {
       int mt, nt;
-      tile_coords(t, p.m_tiles, p.n_tiles, p.group_m, mt, nt);
+      const int sp = u / num_tiles;
+      tile_coords(u - sp * num_tiles, p.m_tiles, p.n_tiles, p.group_m, mt, nt);
+      float* part = p.part + (long)sp * p.M * p.N;
       const int m = mt * 256 + (int)rank * 128 + row_in_tile;
       const int n0 = nt * 256 + sub * COLS;
       if constexpr (KIND == GATED) {
@@ -495,6 +529,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
 #pragma unroll 1
         for (int sg = 0; sg < 3; ++sg) {
           if (p.seg_rows[sg] == 0) continue;
+          float* gp = p.gate_part + ((long)(sg * p.splits + sp) * 4 * p.n_tiles + nt * 4 + sub) * p.M + m;
+          int lo, hi;
+          seg_range(sp, sg, lo, hi);
+          if (lo == hi) {  // none of this modality in this split
+            if (p.gate_grad && in) *gp = 0.f;
+            continue;
+          }
           const float gate = in ? __ldg(p.mod + (long)(sg * 6 + p.gate_slot) * p.D + m) : 0.f;
           if (!wait_full()) break;
           const uint32_t tb = tmem_base + lane_off + (uint32_t)(acc * 256 + sub * COLS);
@@ -517,14 +558,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
             for (int j = 0; j < 16; ++j) sum[c + j] = fmaf(gate, v[j], sum[c + j]);
           }
           release();
-          if (p.gate_grad && in) p.gate_part[((long)sg * 4 * p.n_tiles + nt * 4 + sub) * p.M + m] = dot;
+          if (p.gate_grad && in) *gp = dot;
         }
         if (!ok) break;
         if (p.gate_grad) {
           __syncwarp();
           if (lane == 0) mbar_arrive(w_empty);
         }
-        if (p.out != nullptr) {
+        if (p.out != nullptr && p.splits > 1) {
+          store_part<COLS>(part, p.N, n0, m, p.M, sum);
+        } else if (p.out != nullptr) {
 #pragma unroll
           for (int c = 0; c < COLS; c += 16) {
             uint32_t w[8];
@@ -533,14 +576,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
           }
         }
       } else {
-        if (!wait_full()) break;
+        int lo, hi;
+        seg_range(sp, 0, lo, hi);
+        if (lo < hi && !wait_full()) break;
         const uint32_t tb = tmem_base + lane_off + (uint32_t)(acc * 256);
-        // the accumulator is handed back before the tile's stores: the release
-        // at cluster scope waits for every store before it
+        // the accumulator is handed back before the tile's stores
         if constexpr (KIND == FFN) {
           epi_ffn(p, tb, m, nt, sub, release);
         } else if constexpr (KIND == QKNORM) {
           epi_qknorm(p, tb + sub * COLS, m, n0, freq, axis, wacc + (warp - 2) * 256, release);
+        } else if (p.splits > 1) {
+          float v[COLS];
+          if (lo < hi) {
+#pragma unroll
+            for (int c = 0; c < COLS; c += 32) ld_chunk(tb + sub * COLS + c, v + c);
+            tmem_wait_ld();
+            release();
+          } else {
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) v[c] = 0.f;
+          }
+          store_part<COLS>(part, p.N, n0, m, p.M, v);
         } else {
           uint32_t w[COLS / 2];
 #pragma unroll
@@ -582,6 +638,48 @@ int max_cta_pairs() {
   return n < 128 ? n : 128;
 }
 
+// Splitting the contraction of a product with few output tiles.  In units of
+// one k block's MMAs (about 0.3 us): the longest pair's blocks, and for more
+// than one split a kernel (4 us) and the partials through memory.  Measured
+// at 5,376 x 28,672 over 512 rows (42 tiles for 74 pairs): see the case in the
+// launchers below.
+constexpr size_t SPLIT_BYTES = 48u << 20;  // of the partials, at most
+int plan_splits(int M, int N, int num_kb) {
+  const int tiles = (M + 255) / 256 * ((N + 255) / 256), pairs = max_cta_pairs();
+  if (tiles >= 2 * pairs) return 1;
+  int best = 1;
+  double best_t = (double)((tiles + pairs - 1) / pairs) * num_kb;
+  for (int s = 2; s <= 32 && s * 2 <= num_kb && (size_t)s * M * N * 4 <= SPLIT_BYTES; ++s) {
+    const double t = (double)((tiles * s + pairs - 1) / pairs) * ((num_kb + s - 1) / s) + 14.0 +
+                     (double)s * M * N * 8 / 1.8e6;
+    if (t < best_t) {
+      best = s;
+      best_t = t;
+    }
+  }
+  return best;
+}
+size_t split_bytes(int M, int N, int num_kb) {
+  const int s = plan_splits(M, N, num_kb);
+  return s > 1 ? (size_t)s * M * N * 4 : 0;
+}
+
+// out [n] = bf16(sum of part [splits][n]), n a multiple of 8
+__global__ void __launch_bounds__(256) sum_splits_kernel(const float* __restrict__ part, int splits, long n,
+                                                         bf16* __restrict__ out) {
+  for (long i = (blockIdx.x * 256L + threadIdx.x) * 8; i < n; i += gridDim.x * 2048L) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    for (int s = 0; s < splits; ++s) {
+      const float4* src = reinterpret_cast<const float4*>(part + s * n + i);
+      const float4 x = __ldcs(src), y = __ldcs(src + 1);
+      a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
+      b = make_float4(b.x + y.x, b.y + y.y, b.z + y.z, b.w + y.w);
+    }
+    *reinterpret_cast<uint4*>(out + i) =
+        make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+  }
+}
+
 template <int KIND>
 cudaError_t launch(const Maps& maps, Params p, cudaStream_t stream) {
   static unsigned long long attr_done = 0;
@@ -593,10 +691,15 @@ cudaError_t launch(const Maps& maps, Params p, cudaStream_t stream) {
   // bands of eight row tiles: a wave of 74 tiles is then about 8 x 9, whose
   // operands (17 panels) are the fewest a wave can read
   p.group_m = p.m_tiles < 8 ? p.m_tiles : 8;
-  const int tiles = p.m_tiles * p.n_tiles;
+  if (p.splits < 1) p.splits = 1;
+  const int units = p.m_tiles * p.n_tiles * p.splits;
   const int max_pairs = max_cta_pairs();
-  const int pairs = tiles < max_pairs ? tiles : max_pairs;
+  const int pairs = units < max_pairs ? units : max_pairs;
   gemm_bwd_kernel<KIND><<<2 * pairs, Cfg<KIND>::THREADS, Cfg<KIND>::BYTES, stream>>>(maps, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.splits == 1 || p.out == nullptr) return e;
+  const long n = (long)p.M * p.N, blocks = (n / 8 + 255) / 256, most = (long)num_sms() * 8;
+  sum_splits_kernel<<<(int)(blocks < most ? blocks : most), 256, 0, stream>>>(p.part, p.splits, n, p.out);
   return cudaGetLastError();
 }
 
@@ -611,7 +714,8 @@ bool map_mn(CUtensorMap* m, const void* base, long rows, long cols, long ld) {
 }  // namespace gemm_bwd
 
 // out [out_rows][N] = A [rows][K] B [K][N] for token rows (rows past `rows`: 0)
-cudaError_t launch_dgrad(const bf16* A, const bf16* B, int rows, int out_rows, int N, int K, bf16* out,
+// (part: split_bytes(out_rows, N, K / 64) of scratch)
+cudaError_t launch_dgrad(const bf16* A, const bf16* B, int rows, int out_rows, int N, int K, bf16* out, float* part,
                          cudaStream_t stream) {
   using namespace gemm_bwd;
   Maps maps;
@@ -625,11 +729,14 @@ cudaError_t launch_dgrad(const bf16* A, const bf16* B, int rows, int out_rows, i
   p.rows = rows;
   p.out = out;
   p.ldo = N;
+  p.splits = plan_splits(out_rows, N, K / gemm_bwd::BK);
+  p.part = part;
   return launch<DGRAD>(maps, p, stream);
 }
 
-// out [M][N] = A [rows][M]^T B [rows][N]
-cudaError_t launch_wgrad(const bf16* A, const bf16* B, int rows, int M, int N, bf16* out, cudaStream_t stream) {
+// out [M][N] = A [rows][M]^T B [rows][N] (part: split_bytes(M, N, L_pad / 64))
+cudaError_t launch_wgrad(const bf16* A, const bf16* B, int rows, int L_pad, int M, int N, bf16* out, float* part,
+                         cudaStream_t stream) {
   using namespace gemm_bwd;
   Maps maps;
   Params p;
@@ -641,16 +748,22 @@ cudaError_t launch_wgrad(const bf16* A, const bf16* B, int rows, int M, int N, b
   p.rows = p.seg_rows[0] = rows;
   p.out = out;
   p.ldo = N;
+  p.splits = plan_splits(M, N, L_pad / gemm_bwd::BK);
+  p.part = part;
   return launch<WGRAD>(maps, p, stream);
 }
 
-int gate_parts(int N) { return 4 * ((N + 255) / 256); }
+// Partials of the gate's gradient for each modality
+int gate_parts(int M, int N, int L_pad) {
+  return 4 * ((N + 255) / 256) * gemm_bwd::plan_splits(M, N, L_pad / gemm_bwd::BK);
+}
 
 // dW [M][N] = sum_m gate_m (.) A_m^T B_m over the modality ranges, and the
-// column-tile partials of the gate's gradient into part [3][gate_parts(N)][M]
+// column-tile partials of the gate's gradient into gate_part [3][gate_parts][M]
 // (W, the weight behind the gate: null: none; out == nullptr: no weight gradient)
-cudaError_t launch_wgrad_gated(const bf16* A, const bf16* B, const int* start, const int* count, int M, int N,
-                               const float* mod, int gate_slot, const bf16* W, bf16* out, float* part,
+// (part: split_bytes(M, N, L_pad / 64))
+cudaError_t launch_wgrad_gated(const bf16* A, const bf16* B, const int* start, const int* count, int L_pad, int M, int N,
+                               const float* mod, int gate_slot, const bf16* W, bf16* out, float* gate_part, float* part,
                                cudaStream_t stream) {
   using namespace gemm_bwd;
   Maps maps;
@@ -673,7 +786,9 @@ cudaError_t launch_wgrad_gated(const bf16* A, const bf16* B, const int* start, c
   p.D = M;
   p.gate_grad = W != nullptr;
   if (W != nullptr && !map_k(&maps.w, W, M, N, N)) return cudaErrorInvalidValue;
-  p.gate_part = part;
+  p.gate_part = gate_part;
+  p.splits = plan_splits(M, N, L_pad / gemm_bwd::BK);
+  p.part = part;
   return launch<GATED>(maps, p, stream);
 }
 

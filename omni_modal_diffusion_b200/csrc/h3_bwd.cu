@@ -1,5 +1,7 @@
 // C ABI of the block's backward pass (declarations and contracts:
 // include/h3.h), included by h3_api.cu, whose checks it uses.
+#include <initializer_list>
+
 #include "backward.cu"
 #include "gemm_bwd.cu"
 #include "attention_bwd.cu"
@@ -21,13 +23,39 @@ struct Carve {
 
 struct GatedWs {  // h3_gated_residual_backward and the outer half of h3_ffn_swiglu_backward
   bf16 *plain, *gated;
-  float* part;
+  float *gate_part, *split;  // split: partials of whichever product is being split
 };
-GatedWs carve_gated(Carve& c, const h3_dims* d, int L_pad, int K) {
+size_t max_of(std::initializer_list<size_t> v) {
+  size_t m = 0;
+  for (size_t x : v) m = x > m ? x : m;
+  return m;
+}
+GatedWs carve_gated(Carve& c, const h3_dims* d, int L_pad, int K, size_t more_split) {
+  using gemm_bwd::split_bytes;
   GatedWs w;
   w.plain = c.take<bf16>((size_t)L_pad * d->D);
   w.gated = c.take<bf16>((size_t)L_pad * d->D);
-  w.part = c.take<float>((size_t)3 * gate_parts(K) * d->D);
+  w.gate_part = c.take<float>((size_t)3 * gate_parts(d->D, K, L_pad) * d->D);
+  w.split = c.take<float>(max_of({split_bytes(d->D, K, L_pad / 64), more_split}) / 4);
+  return w;
+}
+GatedWs carve_out(Carve& c, const h3_dims* d, int L_pad) {
+  return carve_gated(c, d, L_pad, d->I, gemm_bwd::split_bytes(L_pad, d->I, d->D / 64));
+}
+GatedWs carve_ffn(Carve& c, const h3_dims* d, int L_pad) {
+  return carve_gated(c, d, L_pad, d->F, max_of({gemm_bwd::split_bytes(L_pad, d->D, 2 * d->F / 64),
+                                                gemm_bwd::split_bytes(2 * d->F, d->D, L_pad / 64)}));
+}
+struct QkvWs {
+  bf16* dqkv;
+  float *norm_part, *split;
+};
+QkvWs carve_qkv(Carve& c, const h3_dims* d, int L_pad) {
+  using gemm_bwd::split_bytes;
+  QkvWs w;
+  w.dqkv = c.take<bf16>((size_t)L_pad * 3 * d->I);
+  w.norm_part = c.take<float>((size_t)QKNORM_PARTS * 2 * 128);
+  w.split = c.take<float>(max_of({split_bytes(L_pad, d->D, 3 * d->I / 64), split_bytes(3 * d->I, d->D, L_pad / 64)}) / 4);
   return w;
 }
 
@@ -51,10 +79,10 @@ cudaError_t gated_weight_grads(const h3_dims* dims, const h3_ranges* r, const Ga
                                const h3_bf16* W, const float* mod, int slot, h3_bf16* dW, h3_bf16* dmod,
                                cudaStream_t st) {
   if (!dW && !dmod) return cudaSuccess;
-  cudaError_t e = launch_wgrad_gated(w.plain, B, r->start, r->count, dims->D, K, mod, slot, dmod ? b16(W) : nullptr,
-                                     b16(dW), w.part, st);
+  cudaError_t e = launch_wgrad_gated(w.plain, B, r->start, r->count, r->L_pad, dims->D, K, mod, slot,
+                                     dmod ? b16(W) : nullptr, b16(dW), w.gate_part, w.split, st);
   if (e != cudaSuccess || !dmod) return e;
-  return launch_gate_reduce(w.part, gate_parts(K), r->count, dims->D, slot, b16(dmod), st);
+  return launch_gate_reduce(w.gate_part, gate_parts(dims->D, K, r->L_pad), r->count, dims->D, slot, b16(dmod), st);
 }
 
 }  // namespace
@@ -66,14 +94,11 @@ size_t h3_backward_workspace_bytes(const h3_dims* dims, int L_pad, int op) {
   Carve c(nullptr);
   switch (op) {
     case H3_BWD_ADALN: c.take<float>((size_t)adaln_bwd_parts(dims->D) * 2 * dims->D); break;
-    case H3_BWD_QKV:
-      c.take<bf16>((size_t)L_pad * 3 * dims->I);
-      c.take<float>((size_t)QKNORM_PARTS * 2 * 128);
-      break;
+    case H3_BWD_QKV: carve_qkv(c, dims, L_pad); break;
     case H3_BWD_ATTENTION: c.take<float>((size_t)2 * dims->H * L_pad); break;
-    case H3_BWD_GATED_RESIDUAL: carve_gated(c, dims, L_pad, dims->I); break;
+    case H3_BWD_GATED_RESIDUAL: carve_out(c, dims, L_pad); break;
     case H3_BWD_FFN:
-      carve_gated(c, dims, L_pad, dims->F);
+      carve_ffn(c, dims, L_pad);
       c.take<bf16>((size_t)L_pad * 3 * dims->F);
       break;
     default: return 0;
@@ -126,20 +151,19 @@ int h3_qkv_qknorm_mrope_backward(const h3_dims* dims, const h3_ranges* ranges, c
   const int D = dims->D, I = dims->I, L = ranges->L, Lp = ranges->L_pad;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Carve c(ws);
-  bf16* dqkv = c.take<bf16>((size_t)Lp * 3 * I);
-  float* part = c.take<float>((size_t)QKNORM_PARTS * 2 * 128);
+  const QkvWs w = carve_qkv(c, dims, Lp);
   const int rope[3] = {dims->rope_t, dims->rope_h, dims->rope_w};
   int n_parts = 0;
   cudaError_t e = launch_qknorm_bwd(b16(xm), b16(Wqkv), b16(dq), b16(dk), b16(qn_w), b16(kn_w), pos, L, Lp, D, I, rope,
-                                    dims->theta, dims->eps_qk, dqkv, part, &n_parts, st);
+                                    dims->theta, dims->eps_qk, w.dqkv, w.norm_part, &n_parts, st);
   if (e != cudaSuccess) return cuda_fail(e, "h3_qkv_qknorm_mrope_backward: norm and RoPE");
-  e = launch_dv_rows(b16(dv), dims->H, L, Lp, dqkv, st);
+  e = launch_dv_rows(b16(dv), dims->H, L, Lp, w.dqkv, st);
   if (e != cudaSuccess) return cuda_fail(e, "h3_qkv_qknorm_mrope_backward: dv");
-  e = launch_norm_weight_reduce(part, n_parts, b16(dqn_w), b16(dkn_w), st);
+  e = launch_norm_weight_reduce(w.norm_part, n_parts, b16(dqn_w), b16(dkn_w), st);
   if (e != cudaSuccess) return cuda_fail(e, "h3_qkv_qknorm_mrope_backward: norm weights");
-  e = launch_dgrad(dqkv, b16(Wqkv), L, Lp, D, 3 * I, b16(dxm), st);
+  e = launch_dgrad(w.dqkv, b16(Wqkv), L, Lp, D, 3 * I, b16(dxm), w.split, st);
   if (e != cudaSuccess) return cuda_fail(e, "h3_qkv_qknorm_mrope_backward: dxm");
-  if (dWqkv) e = launch_wgrad(dqkv, b16(xm), L, 3 * I, D, b16(dWqkv), st);
+  if (dWqkv) e = launch_wgrad(w.dqkv, b16(xm), L, Lp, 3 * I, D, b16(dWqkv), w.split, st);
   if (e != cudaSuccess) return cuda_fail(e, "h3_qkv_qknorm_mrope_backward: dWqkv");
   return ok();
 }
@@ -219,11 +243,11 @@ int h3_gated_residual_backward(const h3_dims* dims, const h3_ranges* ranges, con
   const int D = dims->D, I = dims->I, L = ranges->L, slot = 3 * branch + 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Carve c(ws);
-  const GatedWs w = carve_gated(c, dims, ranges->L_pad, I);
+  const GatedWs w = carve_out(c, dims, ranges->L_pad);
   cudaError_t e = launch_gate_cast(dx, mod, slot, ranges->start, ranges->count, L, D, dWo || dmod ? w.plain : nullptr,
                                    w.gated, st);
   if (e != cudaSuccess) return cuda_fail(e, "h3_gated_residual_backward: gate");
-  e = launch_dgrad(w.gated, b16(Wo), L, ranges->L_pad, I, D, b16(d_o), st);
+  e = launch_dgrad(w.gated, b16(Wo), L, ranges->L_pad, I, D, b16(d_o), w.split, st);
   if (e != cudaSuccess) return cuda_fail(e, "h3_gated_residual_backward: do");
   e = gated_weight_grads(dims, ranges, w, b16(o), I, Wo, mod, slot, dWo, dmod, st);
   if (e != cudaSuccess) return cuda_fail(e, "h3_gated_residual_backward: dWo");
@@ -249,7 +273,7 @@ int h3_ffn_swiglu_backward(const h3_dims* dims, const h3_ranges* ranges, const f
   const int D = dims->D, F = dims->F, L = ranges->L, Lp = ranges->L_pad, slot = 5;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Carve c(ws);
-  const GatedWs w = carve_gated(c, dims, Lp, F);
+  const GatedWs w = carve_ffn(c, dims, Lp);
   bf16* h = c.take<bf16>((size_t)Lp * 3 * F);
   bf16* dgu = h + (size_t)Lp * F;
   cudaError_t e = launch_gate_cast(dx, mod, slot, ranges->start, ranges->count, L, D, dWd || dmod ? w.plain : nullptr,
@@ -257,9 +281,9 @@ int h3_ffn_swiglu_backward(const h3_dims* dims, const h3_ranges* ranges, const f
   if (e != cudaSuccess) return cuda_fail(e, "h3_ffn_swiglu_backward: gate");
   e = launch_ffn_bwd(b16(xm), w.gated, b16(Wgu), b16(Wd), L, D, F, h, dgu, st);
   if (e != cudaSuccess) return cuda_fail(e, "h3_ffn_swiglu_backward: hidden state");
-  e = launch_dgrad(dgu, b16(Wgu), L, Lp, D, 2 * F, b16(dxm), st);
+  e = launch_dgrad(dgu, b16(Wgu), L, Lp, D, 2 * F, b16(dxm), w.split, st);
   if (e != cudaSuccess) return cuda_fail(e, "h3_ffn_swiglu_backward: dxm");
-  if (dWgu) e = launch_wgrad(dgu, b16(xm), L, 2 * F, D, b16(dWgu), st);
+  if (dWgu) e = launch_wgrad(dgu, b16(xm), L, Lp, 2 * F, D, b16(dWgu), w.split, st);
   if (e != cudaSuccess) return cuda_fail(e, "h3_ffn_swiglu_backward: dWgu");
   e = gated_weight_grads(dims, ranges, w, h, F, Wd, mod, slot, dWd, dmod, st);
   if (e != cudaSuccess) return cuda_fail(e, "h3_ffn_swiglu_backward: dWd");
