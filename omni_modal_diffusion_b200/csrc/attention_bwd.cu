@@ -5,9 +5,8 @@
 //   dQ = c dS K,  dK = c dS^T Q.
 // The probabilities are recomputed, never stored.
 //
-// Two kernels instead of one: attention_bwd_kv_kernel owns a key tile and walks
-// the queries (dK, dV), attention_bwd_q_kernel owns a query tile and walks the
-// keys (dQ).  S and dP are taken twice, seven tile products instead of five,
+// Two passes instead of one: a CTA owns a key tile and walks the queries (dK,
+// dV) or a query tile and walks the keys (dQ).  S and dP are taken twice, seven tile products instead of five,
 // but each result then lives in one CTA's TMEM: no fp32 dQ in memory, no
 // atomics (the same call gives the same bits), and P^T and dS go from the
 // registers that computed them to TMEM as the next product's A operand.  One
@@ -45,6 +44,7 @@ __global__ void __launch_bounds__(256) attention_delta_kernel(const bf16* __rest
                                                               const float* __restrict__ lse, int H, int L, int L_pad,
                                                               float* __restrict__ nlse2, float* __restrict__ ndelta) {
   const long total = (long)L_pad * H * 16;
+  chain_wait();
   for (long i = blockIdx.x * 256L + threadIdx.x; i < total; i += gridDim.x * 256L) {
     const long rh = i >> 4;
     const int row = (int)(rh / H), h = (int)(rh - (long)row * H);
@@ -162,16 +162,21 @@ struct KvLayout {
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
 
-__global__ void __launch_bounds__(THREADS, 1)
-    attention_bwd_kv_kernel(const __grid_constant__ BwdMaps maps, const float* __restrict__ nlse2,
-                            const float* __restrict__ ndelta, int L, int L_pad, float scale, float scale_log2,
-                            bf16* __restrict__ dk, bf16* __restrict__ dv) {
+struct BwdArgs {
+  const bf16 *q, *d;
+  const float *nlse2, *ndelta;
+  int H, L, L_pad;
+  float scale, scale_log2;
+  bf16 *dq, *dk, *dv;
+};
+
+__device__ __forceinline__ void key_tile(const BwdMaps& maps, const BwdArgs& p, int tile, int h, uint8_t* smem) {
+  const float *nlse2 = p.nlse2, *ndelta = p.ndelta;
+  const int L = p.L, L_pad = p.L_pad;
+  const float scale = p.scale, scale_log2 = p.scale_log2;
+  bf16 *dk = p.dk, *dv = p.dv;
   using Y = KvLayout;
   constexpr int QS = Y::QS;
-  // seven tiles leave no room to align the base by hand: the swizzled tiles
-  // need 1 KB alignment, which the declaration asks for and the check below holds
-  extern __shared__ __align__(1024) uint8_t smem_kv[];
-  uint8_t* smem = smem_kv;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Y::BAR);
   uint64_t* kv_full = bars + 0;
   uint64_t* q_full = bars + 1;    // [3]
@@ -189,7 +194,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* drain = bars + 21;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 22);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int key0 = blockIdx.x * TILE, h = blockIdx.y;
+  const int key0 = tile * TILE;
   const int n_q = (L + TILE - 1) / TILE;
   if (key0 >= L) {  // a tile of padding rows
     for (int i = threadIdx.x; i < TILE * 16; i += THREADS) {
@@ -197,10 +202,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       reinterpret_cast<uint4*>(dk)[at] = make_uint4(0, 0, 0, 0);
       reinterpret_cast<uint4*>(dv)[at] = make_uint4(0, 0, 0, 0);
     }
-    return;
-  }
-  if (smem_u32(smem) & 1023u) {
-    if (threadIdx.x == 0) atomicCAS(&g_h3_device_error, 0, 1);
     return;
   }
   if (threadIdx.x == 0) {
@@ -317,11 +318,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       ok = mbar_wait_warp(&st_full[i & 1], (i >> 1) & 1) && mbar_wait_warp(s_full, i & 1);
       if (!ok) break;
       tc_fence_after();
-      float p[2][16];
+      float pr[2][16];
       uint32_t pk[2][8];
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh)
-        tmem_ld_16x256b_x4(tS + ((uint32_t)(hh * 16) << 16), reinterpret_cast<uint32_t*>(p[hh]));
+        tmem_ld_16x256b_x4(tS + ((uint32_t)(hh * 16) << 16), reinterpret_cast<uint32_t*>(pr[hh]));
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
@@ -332,10 +333,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint64_t nl2 = f2_pack(nl.x, nl.y);
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          exp2_pair(p[hh] + c * 4, sc2, nl2);
-          exp2_pair(p[hh] + c * 4 + 2, sc2, nl2);
-          pk[hh][c * 2] = pack_bf16x2(p[hh][c * 4], p[hh][c * 4 + 1]);
-          pk[hh][c * 2 + 1] = pack_bf16x2(p[hh][c * 4 + 2], p[hh][c * 4 + 3]);
+          exp2_pair(pr[hh] + c * 4, sc2, nl2);
+          exp2_pair(pr[hh] + c * 4 + 2, sc2, nl2);
+          pk[hh][c * 2] = pack_bf16x2(pr[hh][c * 4], pr[hh][c * 4 + 1]);
+          pk[hh][c * 2 + 1] = pack_bf16x2(pr[hh][c * 4 + 2], pr[hh][c * 4 + 3]);
         }
       }
       ok = mbar_wait_warp(dp_full, i & 1);
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int e = 0; e < 4; e += 2) {
             const int j = c * 4 + e;
             float a, b;
-            f2_unpack(f2_mul(f2_pack(p[hh][j], p[hh][j + 1]), f2_add(f2_pack(dp[hh][j], dp[hh][j + 1]), nd2)), a, b);
+            f2_unpack(f2_mul(f2_pack(pr[hh][j], pr[hh][j + 1]), f2_add(f2_pack(dp[hh][j], dp[hh][j + 1]), nd2)), a, b);
             pk[hh][c * 2 + e / 2] = pack_bf16x2(a, b);
           }
       }
@@ -412,8 +413,8 @@ struct QLayout {
   static constexpr int KS = 4, VS = 2;  // K stages: K(j) for dQ(j) while S(j + 2) reads K(j + 2)
   static constexpr int K = 0, V = KS * TILE_BYTES;
   static constexpr int BAR = V + VS * TILE_BYTES;
-  static constexpr int BYTES = BAR + 256 + 1024;
-  static_assert(BYTES <= 232448, "shared memory per CTA");
+  static constexpr int BYTES = BAR + 256;
+  static_assert(BYTES <= KvLayout::BYTES, "shared memory per CTA");
 };
 
 // D = A B^T over d = 128: A bf16 in TMEM, B a K-major 128 x 128 tile
@@ -425,15 +426,13 @@ __device__ __forceinline__ void mma_tmem_abt(uint32_t d_tmem, uint32_t a_tmem, u
                      kk != 0 ? 1u : 0u);
 }
 
-__global__ void __launch_bounds__(THREADS, 1)
-    attention_bwd_q_kernel(const __grid_constant__ BwdMaps maps, const bf16* __restrict__ q, const bf16* __restrict__ d,
-                           const float* __restrict__ nlse2, const float* __restrict__ ndelta, int L, int L_pad, int H,
-                           float scale, float scale_log2, bf16* __restrict__ dq) {
+__device__ __forceinline__ void query_tile(const BwdMaps& maps, const BwdArgs& p, int tile, int h, uint8_t* smem) {
+  const bf16 *q = p.q, *d = p.d;
+  const int L = p.L, L_pad = p.L_pad, H = p.H;
+  const float scale = p.scale, scale_log2 = p.scale_log2;
+  bf16* dq = p.dq;
   using Y = QLayout;
   constexpr int KS = Y::KS, VS = Y::VS;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Y::BAR);
   uint64_t* q_ready = bars + 0;      // Q and dO in TMEM
   uint64_t* k_full = bars + 1;       // [KS]
@@ -448,7 +447,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* drain = s_full + 5;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 6);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int row0 = blockIdx.x * TILE, h = blockIdx.y;
+  const int row0 = tile * TILE;
   const int n_k = (L + TILE - 1) / TILE;
   if (row0 >= L) {  // a tile of padding rows
     for (int i = threadIdx.x; i < TILE * 16; i += THREADS)
@@ -553,26 +552,26 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(q_ready);
     }
-    const float nl = nlse2[(long)h * L_pad + row0 + r], nd = ndelta[(long)h * L_pad + row0 + r];
+    const float nl = p.nlse2[(long)h * L_pad + row0 + r], nd = p.ndelta[(long)h * L_pad + row0 + r];
     const uint64_t sc2 = f2_pack(scale_log2, scale_log2), nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
     bool ok = true;
     for (int j = 0; j < n_k; ++j) {
       ok = mbar_wait_warp(s_full, j & 1);
       if (!ok) break;
       tc_fence_after();
-      float p[32], dp[32];
-      tmem_ld32(tS, reinterpret_cast<uint32_t*>(p));
+      float pr[32], dp[32];
+      tmem_ld32(tS, reinterpret_cast<uint32_t*>(pr));
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(s_read);
 #pragma unroll
-      for (int c = 0; c < 32; c += 2) exp2_pair(p + c, sc2, nl2);
+      for (int c = 0; c < 32; c += 2) exp2_pair(pr + c, sc2, nl2);
       const int valid = L - j * TILE - g * 32;
       if (valid < 32) {
 #pragma unroll
         for (int c = 0; c < 32; ++c)
-          if (c >= valid) p[c] = 0.f;
+          if (c >= valid) pr[c] = 0.f;
       }
       ok = mbar_wait_warp(dp_full, j & 1);
       if (!ok) break;
@@ -583,7 +582,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int c = 0; c < 32; c += 2) {
         float a, b;
-        f2_unpack(f2_mul(f2_pack(p[c], p[c + 1]), f2_add(f2_pack(dp[c], dp[c + 1]), nd2)), a, b);
+        f2_unpack(f2_mul(f2_pack(pr[c], pr[c + 1]), f2_add(f2_pack(dp[c], dp[c + 1]), nd2)), a, b);
         pk[c / 2] = pack_bf16x2(a, b);
       }
       // the warp's own 32 columns of dP are read: dS over the first 16
@@ -609,6 +608,27 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
+// CTAs [0, n H) take the key tiles, which are the longer work, the others the
+// query tiles: one launch, and one tail instead of two.
+__global__ void __launch_bounds__(THREADS, 1)
+    attention_bwd_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs p, int n) {
+  // seven tiles leave no room to align the base by hand: the swizzled tiles
+  // need 1 KB alignment, which the declaration asks for and this check holds
+  extern __shared__ __align__(1024) uint8_t smem_bwd[];
+  chain_wait();
+  if (smem_u32(smem_bwd) & 1023u) {
+    if (threadIdx.x == 0) atomicCAS(&g_h3_device_error, 0, 1);
+    return;
+  }
+  int b = blockIdx.x;
+  if (b < n * p.H) {
+    key_tile(maps, p, b % n, b / n, smem_bwd);
+  } else {
+    b -= n * p.H;
+    query_tile(maps, p, b % n, b / n, smem_bwd);
+  }
+}
+
 // [H][L_pad][128] heads as 64 x 128-row boxes whose rows end at L
 bool make_tmap_heads(CUtensorMap* map, const void* base, int H, int L, int L_pad) {
   gemm_detail::EncodeTiledFn fn = gemm_detail::encode_fn();
@@ -629,10 +649,8 @@ cudaError_t launch_attention_bwd(const bf16* q, const bf16* k, const bf16* v, co
                                  const bf16* d, int H, int L, int L_pad, float scale, float scale_log2, bf16* dq,
                                  bf16* dk, bf16* dv, float* ws, cudaStream_t stream) {
   using namespace attn_bwd;
-  static unsigned long long kv_done = 0, q_done = 0;
-  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(attention_bwd_kv_kernel), KvLayout::BYTES, &kv_done);
-  if (e != cudaSuccess) return e;
-  e = ensure_smem_attr(reinterpret_cast<const void*>(attention_bwd_q_kernel), QLayout::BYTES, &q_done);
+  static unsigned long long done = 0;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(attention_bwd_kernel), KvLayout::BYTES, &done);
   if (e != cudaSuccess) return e;
   BwdMaps maps;
   if (!make_tmap_heads(&maps.q, q, H, L, L_pad) || !make_tmap_heads(&maps.k, k, H, L, L_pad) ||
@@ -642,14 +660,12 @@ cudaError_t launch_attention_bwd(const bf16* q, const bf16* k, const bf16* v, co
   float* ndelta = ws + (size_t)H * L_pad;
   const long pieces = (long)L_pad * H * 16;
   const long blocks = (pieces + 255) / 256, most = (long)num_sms() * 16;
-  attention_delta_kernel<<<(int)(blocks < most ? blocks : most), 256, 0, stream>>>(o, d, lse, H, L, L_pad, nlse2,
-                                                                                   ndelta);
-  const dim3 grid(L_pad / attn_detail::TILE, H);
-  attention_bwd_kv_kernel<<<grid, THREADS, KvLayout::BYTES, stream>>>(maps, nlse2, ndelta, L, L_pad, scale, scale_log2,
-                                                                      dk, dv);
-  attention_bwd_q_kernel<<<grid, THREADS, QLayout::BYTES, stream>>>(maps, q, d, nlse2, ndelta, L, L_pad, H, scale,
-                                                                    scale_log2, dq);
-  return cudaGetLastError();
+  e = launch_chained(attention_delta_kernel, dim3((int)(blocks < most ? blocks : most)), 256, 0, stream, o, d, lse, H, L,
+                     L_pad, nlse2, ndelta);
+  if (e != cudaSuccess) return e;
+  const int n = L_pad / attn_detail::TILE;
+  const BwdArgs args{q, d, nlse2, ndelta, H, L, L_pad, scale, scale_log2, dq, dk, dv};
+  return launch_chained(attention_bwd_kernel, dim3(2 * n * H), THREADS, KvLayout::BYTES, stream, maps, args, n);
 }
 
 }  // namespace h3

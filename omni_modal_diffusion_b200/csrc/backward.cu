@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(AB_MAX_THREADS) adaln_bwd_kernel(
   __shared__ uint64_t full[AB_STAGES];
   const int nv = D / 4, T = blockDim.x;
   const int n_chunks = ch.first[3];
+  chain_wait();
   if ((int)blockIdx.x >= n_chunks) {  // padding rows
     for (long row = L + blockIdx.x - n_chunks; row < L_pad; row += gridDim.x - n_chunks)
       for (int i = threadIdx.x; i < nv; i += T)
@@ -197,19 +198,19 @@ __global__ void __launch_bounds__(AB_MAX_THREADS) adaln_bwd_kernel(
 }
 
 // ------------------------------------------------------------ partial sums
-// out[m * out_stride + c] = bf16(sum of part[p * stride + c] over p in
-// [begin[m], end[m])), c < cols.  A CTA takes 32
-// columns; its eight warps take every eighth partial and their sums are added
-// in order.
+// out[m][c] = bf16(sum of part[p * stride + m * offset + c] over p in [begin[m],
+// end[m])), c < cols, for the blockIdx.y-th m.  A CTA takes 32 columns; its
+// eight warps take every eighth partial and their sums are added in order.
 struct Parts {
   int begin[3], end[3];
+  bf16* out[3];  // null: not wanted
 };
-__global__ void __launch_bounds__(256) reduce_parts_kernel(const float* __restrict__ part, Parts pp, long stride,
-                                                           int cols, bf16* __restrict__ out, long out_stride) {
-  __shared__ float acc[8][32];
-  const int m = blockIdx.y, c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x / 32;
+__device__ __forceinline__ void reduce_parts(const float* __restrict__ part, const Parts& pp, int m, long stride,
+                                             long offset, int cols, int block, float (*acc)[32]) {
+  const int c = block * 32 + (threadIdx.x & 31), w = threadIdx.x / 32;
+  part += m * offset;
   float s = 0.f;
-  if (c < cols) {
+  if (c < cols && pp.out[m] != nullptr) {
     int p = pp.begin[m] + w;
     const int end = pp.end[m];
     for (; p + 24 < end; p += 32) {
@@ -221,11 +222,45 @@ __global__ void __launch_bounds__(256) reduce_parts_kernel(const float* __restri
   }
   acc[w][threadIdx.x & 31] = s;
   __syncthreads();
-  if (w == 0 && c < cols) {
+  if (w == 0 && c < cols && pp.out[m] != nullptr) {
     float t = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) t += acc[k][threadIdx.x];
-    out[m * out_stride + c] = __float2bfloat16_rn(t);
+    pp.out[m][c] = __float2bfloat16_rn(t);
+  }
+}
+__global__ void __launch_bounds__(256) reduce_parts_kernel(const float* __restrict__ part,
+                                                           const __grid_constant__ Parts pp, long stride, long offset,
+                                                           int cols) {
+  __shared__ float acc[8][32];
+  chain_wait();
+  reduce_parts(part, pp, blockIdx.y, stride, offset, cols, blockIdx.x, acc);
+}
+
+// The end of a split weight gradient of a gated linear: CTAs [0, sum_ctas) add
+// its fp32 partials, dW [n] = bf16(sum over part [splits][n]) (n a multiple of
+// 8), the others the gate's.
+__global__ void __launch_bounds__(256) finish_splits_kernel(const float* __restrict__ part, int splits, long n,
+                                                            bf16* __restrict__ out, int sum_ctas,
+                                                            const float* __restrict__ gate_part,
+                                                            const __grid_constant__ Parts pp, int cols, int gate_ctas) {
+  __shared__ float acc[8][32];
+  chain_wait();
+  const int b = blockIdx.x;
+  if (b >= sum_ctas) {
+    reduce_parts(gate_part, pp, (b - sum_ctas) / gate_ctas, cols, 0, cols, (b - sum_ctas) % gate_ctas, acc);
+    return;
+  }
+  for (long i = (b * 256L + threadIdx.x) * 8; i < n; i += sum_ctas * 2048L) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    for (int s = 0; s < splits; ++s) {
+      const float4* src = reinterpret_cast<const float4*>(part + s * n + i);
+      const float4 u = __ldcs(src), v = __ldcs(src + 1);
+      x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
+      y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
+    }
+    *reinterpret_cast<uint4*>(out + i) =
+        make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
   }
 }
 
@@ -238,6 +273,7 @@ __global__ void __launch_bounds__(256) gate_cast_kernel(const float* __restrict_
                                                         bf16* __restrict__ plain, bf16* __restrict__ gated) {
   const int n8 = D / 8;
   const long total = (long)L * n8;
+  chain_wait();
   for (long i = blockIdx.x * 256L + threadIdx.x; i < total; i += gridDim.x * 256L) {
     const int row = (int)(i / n8), c = (int)(i - (long)row * n8);
     const float4* src = reinterpret_cast<const float4*>(dx + (long)row * D) + 2 * c;
@@ -261,6 +297,7 @@ __global__ void __launch_bounds__(256) dv_rows_kernel(const bf16* __restrict__ d
                                                       bf16* __restrict__ dqkv) {
   const int per_row = H * 16;  // 16-byte pieces
   const long total = (long)L * per_row;
+  chain_wait();
   for (long i = blockIdx.x * 256L + threadIdx.x; i < total; i += gridDim.x * 256L) {
     const int row = (int)(i / per_row), c = (int)(i - (long)row * per_row);
     const int h = c >> 4, j = c & 15;
@@ -296,12 +333,13 @@ cudaError_t launch_adaln_bwd(const float* x, const float* mod, int branch, const
   const int grid = ch.first[3] + pad, vpt = (D / 4 + plan.threads - 1) / plan.threads;
   const int bytes = plan.stages * 10 * D;
   static unsigned long long attr_done[4] = {0, 0, 0, 0};
+  cudaError_t e = cudaSuccess;
 #define H3_ADALN_BWD(V)                                                                                              \
   case V: {                                                                                                          \
     cudaError_t ea = ensure_smem_attr(reinterpret_cast<const void*>(adaln_bwd_kernel<V>), AB_SMEM, &attr_done[V - 1]); \
     if (ea != cudaSuccess) return ea;                                                                                \
-    adaln_bwd_kernel<V><<<grid, plan.threads, bytes, stream>>>(x, mod, branch, dy, dres, dx, rg, ch, L, L_pad, D, eps, \
-                                                               plan.stages, part);                                   \
+    e = launch_chained(adaln_bwd_kernel<V>, dim3(grid), plan.threads, bytes, stream, x, mod, branch, dy, dres, dx, rg, \
+                       ch, L, L_pad, D, eps, plan.stages, part);                                                     \
     break;                                                                                                           \
   }
   switch (vpt) {
@@ -312,7 +350,6 @@ cudaError_t launch_adaln_bwd(const float* x, const float* mod, int branch, const
     default: return cudaErrorInvalidValue;
   }
 #undef H3_ADALN_BWD
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || dmod == nullptr) return e;
   // the branch's shift and scale rows are neighbours in [3][6][D], as their
   // partials are
@@ -320,32 +357,41 @@ cudaError_t launch_adaln_bwd(const float* x, const float* mod, int branch, const
   for (int m = 0; m < 3; ++m) {
     pp.begin[m] = ch.first[m];
     pp.end[m] = ch.first[m + 1];
+    pp.out[m] = dmod + (long)(m * 6 + 3 * branch) * D;
   }
-  reduce_parts_kernel<<<dim3((2 * D + 31) / 32, 3), 256, 0, stream>>>(part, pp, 2L * D, 2 * D,
-                                                                      dmod + (long)3 * branch * D, 6L * D);
-  return cudaGetLastError();
+  return launch_chained(reduce_parts_kernel, dim3((2 * D + 31) / 32, 3), 256, 0, stream, part, pp, 2L * D, 0L, 2 * D);
 }
 
-// dmod[m][gate_slot][:] from part [3][n_parts][D] (modalities without tokens: 0)
-cudaError_t launch_gate_reduce(const float* part, int n_parts, const int* rcount, int D, int gate_slot, bf16* dmod,
-                               cudaStream_t stream) {
+// The gate's slot of dmod from gate_part [3][n_parts][D] (modalities without
+// tokens: 0; dmod null: none), and of a split weight gradient its sum, out [n]
+// from part [splits][n]
+cudaError_t launch_finish_gated(const float* gate_part, int n_parts, const int* rcount, int D, int gate_slot, bf16* dmod,
+                                const float* part, int splits, long n, bf16* out, cudaStream_t stream) {
   Parts pp;
   for (int m = 0; m < 3; ++m) {
     pp.begin[m] = m * n_parts;
     pp.end[m] = rcount[m] > 0 ? (m + 1) * n_parts : m * n_parts;
+    pp.out[m] = dmod ? dmod + (long)(m * 6 + gate_slot) * D : nullptr;
   }
-  reduce_parts_kernel<<<dim3((D + 31) / 32, 3), 256, 0, stream>>>(part, pp, D, D, dmod + (long)gate_slot * D, 6L * D);
-  return cudaGetLastError();
+  const int gate_ctas = (D + 31) / 32;
+  if (splits == 1 || out == nullptr)
+    return dmod ? launch_chained(reduce_parts_kernel, dim3(gate_ctas, 3), 256, 0, stream, gate_part, pp, (long)D, 0L, D)
+                : cudaSuccess;
+  const long blocks = (n / 8 + 255) / 256, most = (long)num_sms() * 8;
+  const int sum_ctas = (int)(blocks < most ? blocks : most);
+  return launch_chained(finish_splits_kernel, dim3(sum_ctas + (dmod ? 3 * gate_ctas : 0)), 256, 0, stream, part, splits,
+                        n, out, sum_ctas, gate_part, pp, D, gate_ctas);
 }
 
-// dqn_w, dkn_w [128] from part [n_parts][2][128]
+// dqn_w, dkn_w [128] from part [n_parts][2][128] (either may be null)
 cudaError_t launch_norm_weight_reduce(const float* part, int n_parts, bf16* dqn_w, bf16* dkn_w, cudaStream_t stream) {
+  if (!dqn_w && !dkn_w) return cudaSuccess;
   Parts pp;
   memset(&pp, 0, sizeof(pp));
-  pp.end[0] = n_parts;
-  if (dqn_w) reduce_parts_kernel<<<dim3(4, 1), 256, 0, stream>>>(part, pp, 256, 128, dqn_w, 0);
-  if (dkn_w) reduce_parts_kernel<<<dim3(4, 1), 256, 0, stream>>>(part + 128, pp, 256, 128, dkn_w, 0);
-  return cudaGetLastError();
+  pp.end[0] = pp.end[1] = n_parts;
+  pp.out[0] = dqn_w;
+  pp.out[1] = dkn_w;
+  return launch_chained(reduce_parts_kernel, dim3(4, 2), 256, 0, stream, part, pp, 256L, 128L, 128);
 }
 
 static int stream_grid(long items) {
@@ -361,13 +407,12 @@ cudaError_t launch_gate_cast(const float* dx, const float* mod, int gate_slot, c
     rg.start[m] = rstart[m];
     rg.count[m] = rcount[m];
   }
-  gate_cast_kernel<<<stream_grid((long)L * D / 8), 256, 0, stream>>>(dx, mod, gate_slot, rg, L, D, plain, gated);
-  return cudaGetLastError();
+  return launch_chained(gate_cast_kernel, dim3(stream_grid((long)L * D / 8)), 256, 0, stream, dx, mod, gate_slot, rg, L,
+                        D, plain, gated);
 }
 
 cudaError_t launch_dv_rows(const bf16* dv, int H, int L, int L_pad, bf16* dqkv, cudaStream_t stream) {
-  dv_rows_kernel<<<stream_grid((long)L * H * 16), 256, 0, stream>>>(dv, H, L, L_pad, dqkv);
-  return cudaGetLastError();
+  return launch_chained(dv_rows_kernel, dim3(stream_grid((long)L * H * 16)), 256, 0, stream, dv, H, L, L_pad, dqkv);
 }
 
 }  // namespace h3

@@ -357,6 +357,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
   cluster_sync();  // barriers of both CTAs initialised before any remote arrival
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  chain_wait();
 
   const int num_tiles = p.m_tiles * p.n_tiles;
   const int num_units = num_tiles * p.splits;
@@ -664,22 +665,6 @@ size_t split_bytes(int M, int N, int num_kb) {
   return s > 1 ? (size_t)s * M * N * 4 : 0;
 }
 
-// out [n] = bf16(sum of part [splits][n]), n a multiple of 8
-__global__ void __launch_bounds__(256) sum_splits_kernel(const float* __restrict__ part, int splits, long n,
-                                                         bf16* __restrict__ out) {
-  for (long i = (blockIdx.x * 256L + threadIdx.x) * 8; i < n; i += gridDim.x * 2048L) {
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-    for (int s = 0; s < splits; ++s) {
-      const float4* src = reinterpret_cast<const float4*>(part + s * n + i);
-      const float4 x = __ldcs(src), y = __ldcs(src + 1);
-      a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
-      b = make_float4(b.x + y.x, b.y + y.y, b.z + y.z, b.w + y.w);
-    }
-    *reinterpret_cast<uint4*>(out + i) =
-        make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
-  }
-}
-
 template <int KIND>
 cudaError_t launch(const Maps& maps, Params p, cudaStream_t stream) {
   static unsigned long long attr_done = 0;
@@ -695,12 +680,13 @@ cudaError_t launch(const Maps& maps, Params p, cudaStream_t stream) {
   const int units = p.m_tiles * p.n_tiles * p.splits;
   const int max_pairs = max_cta_pairs();
   const int pairs = units < max_pairs ? units : max_pairs;
-  gemm_bwd_kernel<KIND><<<2 * pairs, Cfg<KIND>::THREADS, Cfg<KIND>::BYTES, stream>>>(maps, p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || p.splits == 1 || p.out == nullptr) return e;
-  const long n = (long)p.M * p.N, blocks = (n / 8 + 255) / 256, most = (long)num_sms() * 8;
-  sum_splits_kernel<<<(int)(blocks < most ? blocks : most), 256, 0, stream>>>(p.part, p.splits, n, p.out);
-  return cudaGetLastError();
+  return launch_chained(gemm_bwd_kernel<KIND>, dim3(2 * pairs), Cfg<KIND>::THREADS, Cfg<KIND>::BYTES, stream, maps, p);
+}
+
+// the sum of a split product's partials
+cudaError_t finish(const Params& p, cudaStream_t stream) {
+  static const int none[3] = {0, 0, 0};
+  return launch_finish_gated(nullptr, 0, none, 0, 0, nullptr, p.part, p.splits, (long)p.M * p.N, p.out, stream);
 }
 
 // K-major operand: rows x cols, 128-row boxes; MN-major: 64-row boxes
@@ -731,7 +717,8 @@ cudaError_t launch_dgrad(const bf16* A, const bf16* B, int rows, int out_rows, i
   p.ldo = N;
   p.splits = plan_splits(out_rows, N, K / gemm_bwd::BK);
   p.part = part;
-  return launch<DGRAD>(maps, p, stream);
+  const cudaError_t e = launch<DGRAD>(maps, p, stream);
+  return e != cudaSuccess ? e : finish(p, stream);
 }
 
 // out [M][N] = A [rows][M]^T B [rows][N] (part: split_bytes(M, N, L_pad / 64))
@@ -750,7 +737,8 @@ cudaError_t launch_wgrad(const bf16* A, const bf16* B, int rows, int L_pad, int 
   p.ldo = N;
   p.splits = plan_splits(M, N, L_pad / gemm_bwd::BK);
   p.part = part;
-  return launch<WGRAD>(maps, p, stream);
+  const cudaError_t e = launch<WGRAD>(maps, p, stream);
+  return e != cudaSuccess ? e : finish(p, stream);
 }
 
 // Partials of the gate's gradient for each modality
@@ -758,13 +746,14 @@ int gate_parts(int M, int N, int L_pad) {
   return 4 * ((N + 255) / 256) * gemm_bwd::plan_splits(M, N, L_pad / gemm_bwd::BK);
 }
 
-// dW [M][N] = sum_m gate_m (.) A_m^T B_m over the modality ranges, and the
-// column-tile partials of the gate's gradient into gate_part [3][gate_parts][M]
-// (W, the weight behind the gate: null: none; out == nullptr: no weight gradient)
+
+// dW [M][N] = sum_m gate_m (.) A_m^T B_m over the modality ranges (out; null: no
+// weight gradient), and the gate's gradient into its slot of dmod (null: none)
+// by way of gate_part [3][gate_parts][M]; W: the weight behind the gate
 // (part: split_bytes(M, N, L_pad / 64))
 cudaError_t launch_wgrad_gated(const bf16* A, const bf16* B, const int* start, const int* count, int L_pad, int M, int N,
-                               const float* mod, int gate_slot, const bf16* W, bf16* out, float* gate_part, float* part,
-                               cudaStream_t stream) {
+                               const float* mod, int gate_slot, const bf16* W, bf16* out, bf16* dmod, float* gate_part,
+                               float* part, cudaStream_t stream) {
   using namespace gemm_bwd;
   Maps maps;
   Params p;
@@ -784,12 +773,15 @@ cudaError_t launch_wgrad_gated(const bf16* A, const bf16* B, const int* start, c
   p.mod = mod;
   p.gate_slot = gate_slot;
   p.D = M;
-  p.gate_grad = W != nullptr;
-  if (W != nullptr && !map_k(&maps.w, W, M, N, N)) return cudaErrorInvalidValue;
+  p.gate_grad = dmod != nullptr;
+  if (p.gate_grad && !map_k(&maps.w, W, M, N, N)) return cudaErrorInvalidValue;
   p.gate_part = gate_part;
   p.splits = plan_splits(M, N, L_pad / gemm_bwd::BK);
   p.part = part;
-  return launch<GATED>(maps, p, stream);
+  const cudaError_t e = launch<GATED>(maps, p, stream);
+  if (e != cudaSuccess) return e;
+  return launch_finish_gated(gate_part, gate_parts(M, N, L_pad), count, M, gate_slot, dmod, part, p.splits, (long)M * N,
+                             out, stream);
 }
 
 // h [rows][F] and dgu [rows][2F] from xm, dy [rows][D], Wgu [2F][D], Wd [D][F]

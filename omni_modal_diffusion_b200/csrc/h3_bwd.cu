@@ -79,10 +79,8 @@ cudaError_t gated_weight_grads(const h3_dims* dims, const h3_ranges* r, const Ga
                                const h3_bf16* W, const float* mod, int slot, h3_bf16* dW, h3_bf16* dmod,
                                cudaStream_t st) {
   if (!dW && !dmod) return cudaSuccess;
-  cudaError_t e = launch_wgrad_gated(w.plain, B, r->start, r->count, r->L_pad, dims->D, K, mod, slot,
-                                     dmod ? b16(W) : nullptr, b16(dW), w.gate_part, w.split, st);
-  if (e != cudaSuccess || !dmod) return e;
-  return launch_gate_reduce(w.gate_part, gate_parts(dims->D, K, r->L_pad), r->count, dims->D, slot, b16(dmod), st);
+  return launch_wgrad_gated(w.plain, B, r->start, r->count, r->L_pad, dims->D, K, mod, slot, b16(W), b16(dW), b16(dmod),
+                            w.gate_part, w.split, st);
 }
 
 }  // namespace

@@ -144,6 +144,23 @@ cudaError_t launch_silu_bf16(const float* c, long long n, bf16* a, cudaStream_t 
 
 int num_sms();
 
+// Launch a kernel that begins with chain_wait(): its launch, barrier set-up and
+// TMEM allocation overlap the end of the kernel before it on the stream.
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // cudaFuncSetAttribute(func, MaxDynamicSharedMemorySize, bytes) once per
 // device (function attributes are per device context).
 cudaError_t ensure_smem_attr(const void* func, int bytes, unsigned long long* done_mask);

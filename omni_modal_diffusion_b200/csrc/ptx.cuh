@@ -404,6 +404,16 @@ __device__ __forceinline__ void drain_mmas(uint64_t* bar) {
   mbar_wait(bar, 0);
 }
 
+// ------------------------------------------------------------ chained launches
+// A kernel of a chain launched with launch_chained: lets the next one start its
+// CTAs where there is room, and waits until the one before has completed and
+// its writes are visible.  Called by every thread before its first access to
+// memory that another kernel writes or reads.
+__device__ __forceinline__ void chain_wait() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ------------------------------------------------------------ misc
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
