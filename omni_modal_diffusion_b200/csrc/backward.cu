@@ -237,29 +237,47 @@ __global__ void __launch_bounds__(256) reduce_parts_kernel(const float* __restri
   reduce_parts(part, pp, blockIdx.y, stride, offset, cols, blockIdx.x, acc);
 }
 
-// The end of a split weight gradient of a gated linear: CTAs [0, sum_ctas) add
-// its fp32 partials, dW [n] = bf16(sum over part [splits][n]) (n a multiple of
-// 8), the others the gate's.
-__global__ void __launch_bounds__(256) finish_splits_kernel(const float* __restrict__ part, int splits, long n,
-                                                            bf16* __restrict__ out, int sum_ctas,
-                                                            const float* __restrict__ gate_part,
-                                                            const __grid_constant__ Parts pp, int cols, int gate_ctas) {
+// What is left after the products of a backward call: the sums of the split
+// ones, out [n] = bf16(sum over part [splits][n]) (n a multiple of 8), and one
+// reduction of partials (a gate's or the norm weights' gradients)
+struct SplitSum {
+  const float* part;
+  bf16* out;
+  long n;
+  int splits;
+};
+struct FinishArgs {
+  int n_sums, n_reduce;
+  SplitSum sum[3];
+  int first[4];  // CTAs [first[i], first[i + 1]) take sum i, the rest the reduction
+  Parts reduce;
+  const float* reduce_part;
+  long reduce_stride, reduce_offset;
+  int reduce_cols, reduce_ctas;
+};
+__global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ FinishArgs f) {
   __shared__ float acc[8][32];
   chain_wait();
   const int b = blockIdx.x;
-  if (b >= sum_ctas) {
-    reduce_parts(gate_part, pp, (b - sum_ctas) / gate_ctas, cols, 0, cols, (b - sum_ctas) % gate_ctas, acc);
+  if (b >= f.first[f.n_sums]) {
+    const int r = b - f.first[f.n_sums];
+    reduce_parts(f.reduce_part, f.reduce, r / f.reduce_ctas, f.reduce_stride, f.reduce_offset, f.reduce_cols,
+                 r % f.reduce_ctas, acc);
     return;
   }
-  for (long i = (b * 256L + threadIdx.x) * 8; i < n; i += sum_ctas * 2048L) {
+  int k = 0;
+  while (b >= f.first[k + 1]) ++k;
+  const SplitSum& j = f.sum[k];
+  const long step = (f.first[k + 1] - f.first[k]) * 2048L;
+  for (long i = ((b - f.first[k]) * 256L + threadIdx.x) * 8; i < j.n; i += step) {
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-    for (int s = 0; s < splits; ++s) {
-      const float4* src = reinterpret_cast<const float4*>(part + s * n + i);
+    for (int s = 0; s < j.splits; ++s) {
+      const float4* src = reinterpret_cast<const float4*>(j.part + s * j.n + i);
       const float4 u = __ldcs(src), v = __ldcs(src + 1);
       x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
       y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
     }
-    *reinterpret_cast<uint4*>(out + i) =
+    *reinterpret_cast<uint4*>(j.out + i) =
         make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
   }
 }
@@ -362,36 +380,20 @@ cudaError_t launch_adaln_bwd(const float* x, const float* mod, int branch, const
   return launch_chained(reduce_parts_kernel, dim3((2 * D + 31) / 32, 3), 256, 0, stream, part, pp, 2L * D, 0L, 2 * D);
 }
 
-// The gate's slot of dmod from gate_part [3][n_parts][D] (modalities without
-// tokens: 0; dmod null: none), and of a split weight gradient its sum, out [n]
-// from part [splits][n]
-cudaError_t launch_finish_gated(const float* gate_part, int n_parts, const int* rcount, int D, int gate_slot, bf16* dmod,
-                                const float* part, int splits, long n, bf16* out, cudaStream_t stream) {
-  Parts pp;
-  for (int m = 0; m < 3; ++m) {
-    pp.begin[m] = m * n_parts;
-    pp.end[m] = rcount[m] > 0 ? (m + 1) * n_parts : m * n_parts;
-    pp.out[m] = dmod ? dmod + (long)(m * 6 + gate_slot) * D : nullptr;
+// One launch for all of it (none if nothing is left)
+cudaError_t launch_finish(FinishArgs f, cudaStream_t stream) {
+  int ctas = 0;
+  for (int i = 0; i < f.n_sums; ++i) {
+    const long blocks = (f.sum[i].n / 8 + 255) / 256, most = (long)num_sms() * 8;
+    f.first[i] = ctas;
+    ctas += (int)(blocks < most ? blocks : most);
   }
-  const int gate_ctas = (D + 31) / 32;
-  if (splits == 1 || out == nullptr)
-    return dmod ? launch_chained(reduce_parts_kernel, dim3(gate_ctas, 3), 256, 0, stream, gate_part, pp, (long)D, 0L, D)
-                : cudaSuccess;
-  const long blocks = (n / 8 + 255) / 256, most = (long)num_sms() * 8;
-  const int sum_ctas = (int)(blocks < most ? blocks : most);
-  return launch_chained(finish_splits_kernel, dim3(sum_ctas + (dmod ? 3 * gate_ctas : 0)), 256, 0, stream, part, splits,
-                        n, out, sum_ctas, gate_part, pp, D, gate_ctas);
-}
-
-// dqn_w, dkn_w [128] from part [n_parts][2][128] (either may be null)
-cudaError_t launch_norm_weight_reduce(const float* part, int n_parts, bf16* dqn_w, bf16* dkn_w, cudaStream_t stream) {
-  if (!dqn_w && !dkn_w) return cudaSuccess;
-  Parts pp;
-  memset(&pp, 0, sizeof(pp));
-  pp.end[0] = pp.end[1] = n_parts;
-  pp.out[0] = dqn_w;
-  pp.out[1] = dkn_w;
-  return launch_chained(reduce_parts_kernel, dim3(4, 2), 256, 0, stream, part, pp, 256L, 128L, 128);
+  f.first[f.n_sums] = ctas;
+  if (f.n_reduce > 0) {
+    f.reduce_ctas = (f.reduce_cols + 31) / 32;
+    ctas += f.n_reduce * f.reduce_ctas;
+  }
+  return ctas > 0 ? launch_chained(finish_kernel, dim3(ctas), 256, 0, stream, f) : cudaSuccess;
 }
 
 static int stream_grid(long items) {

@@ -1,24 +1,28 @@
 // tcgen05 GEMMs of the block's backward pass, all on CTA pairs (cta_group::2,
 // 256 x 256 output tiles over two SMs, fp32 accumulators in TMEM):
 //
-//   DGRAD   out[t][n] = sum_k A[t][k] B[k][n]: the gradient of a linear's input.
-//           B is the forward weight [out, in] read with its rows as the
-//           contraction, so no transposed copy of a weight exists: its tiles
-//           enter shared memory as they lie (64 columns x 64 rows per TMA box)
-//           and the MMA takes them MN-major.
-//   WGRAD   out[j][n] = sum_t A[t][j] B[t][n]: the gradient of a weight; both
-//           operands MN-major, the contraction over the tokens.
-//   GATED   WGRAD for a linear behind a modality gate (y = gate_m (.) (B W^T)):
-//           one accumulator per modality range, G_m = sum_{t in m} A^T B, then
+//   PRODUCTS  up to three independent products, the tiles of one after those of
+//           another in one persistent launch (one tail instead of three, and
+//           small ones side by side):
+//     input gradient   out[t][n] = sum_k A[t][k] B[k][n].  B is the forward
+//           weight [out, in] read with its rows as the contraction, so no
+//           transposed copy of a weight exists: its tiles enter shared memory
+//           as they lie (64 columns x 64 rows per TMA box) and the MMA takes
+//           them MN-major.
+//     weight gradient  out[j][n] = sum_t A[t][j] B[t][n]: both operands
+//           MN-major, the contraction over the tokens.
+//     gated weight gradient, for a linear behind a modality gate
+//           (y = gate_m (.) (B W^T)): one accumulator per modality range, G_m =
+//           sum_{t in m} A^T B, then
 //             dW[j][n]    = sum_m gate_m[j] G_m[j][n]
 //             dgate_m[j]  = sum_n W[j][n] G_m[j][n]
 //           (the second is sum_t dx[t][j] (B W^T)[t][j] with the order of the
 //           sums exchanged), so the gate's gradient needs neither the branch
 //           output nor another product, and a gate of 0 loses nothing.
-//   QKNORM  x = A W_qk^T (the q, k projection again), and in the epilogue the
+//   QKNORM    x = A W_qk^T (the q, k projection again), and in the epilogue the
 //           backward pass of RoPE and of the per-head RMSNorm.
-//   FFN     gate, up = A Wgu^T and dh = dY Wd in one K loop, and in the epilogue
-//           h = SiLU(g) u and the gradients of g and u.
+//   FFN       gate, up = A Wgu^T and dh = dY Wd in one K loop, and in the
+//           epilogue h = SiLU(g) u and the gradients of g and u.
 //
 // A segment, a ragged length and the padding rows end inside a tile: the tensor
 // maps stop at the last valid token, and TMA reads zeros past it.
@@ -30,34 +34,44 @@ namespace h3 {
 namespace gemm_bwd {
 using gemm_detail::tile_coords;
 
-enum Kind : int { DGRAD = 0, WGRAD = 1, GATED = 2, QKNORM = 3, FFN = 4 };
+enum Kind : int { PRODUCTS = 0, QKNORM = 1, FFN = 2 };
 
+constexpr int MAX_PRODUCTS = 3;
 struct Maps {
-  CUtensorMap a[3], b[3];  // per segment (GATED), else index 0; FFN: a[1], b[1] are dY and Wd
-  CUtensorMap w;           // GATED: W, 128-row boxes
+  // QKNORM: A, B; FFN: xm, Wgu, dY, Wd; PRODUCTS: of each product A and B of
+  // every segment, then W if gated (input and weight gradients 2 each, gated 7)
+  CUtensorMap m[11];
+};
+
+struct Product {
+  int map0;           // its first tensor map
+  int a_mn;           // A MN-major (weight gradients) or K-major
+  int gated, segs;    // gated: three segments, else one
+  int M, N;           // output rows and columns
+  int m_tiles, n_tiles, group_m;
+  int kb[3];          // k blocks of each segment
+  // The contraction in `splits` equal runs of k blocks, each a unit of work of
+  // its own that writes an fp32 partial, part [splits][M][N]; 1: none
+  int splits, units;
+  float* part;
+  bf16* out;          // [M][N]; null (gated only): not wanted
 };
 
 struct Params {
-  int M, N, K;  // output rows and columns; contraction length (unused by WGRAD, GATED)
-  int m_tiles, n_tiles, group_m;
-  // The contraction in `splits` equal runs of k blocks, each a unit of work of
-  // its own that writes an fp32 partial, part [splits][M][N]; 1: none
-  int splits;
-  float* part;
-  int rows;           // valid token rows
-  int seg_rows[3];    // WGRAD: [0] = rows; GATED: tokens of each modality
-  bf16* out;          // DGRAD, WGRAD, GATED (may be null): [M][ldo]
-  long ldo;
-  // GATED
-  const float* mod;   // [3][6][D]
-  int gate_slot, D;
+  int n_products, units, n_maps;
+  Product pr[MAX_PRODUCTS];
+  // the gated product
+  const float* mod;   // [3][6][D], D = its M
+  int gate_slot;
   int gate_grad;      // whether the gate's gradient is wanted
-  float* gate_part;   // [3][splits * 4 n_tiles][M] column-quarter partials of the gate's gradient
+  float* gate_part;   // [3][splits * 4 n_tiles][M] column-quarter partials of it
+  int rows;           // QKNORM, FFN: valid token rows
   // FFN
   bf16* h;            // [.][F]
   bf16* dgu;          // [.][2F]
   int F;
   // QKNORM
+  bf16* dqkv;         // [.][3I]
   const bf16* dq;     // [H][L_pad][128], gradients of the rotated q and k
   const bf16* dk;
   const bf16* qn_w;
@@ -72,19 +86,20 @@ constexpr int BK = 64;
 constexpr int OPERAND = 128 * BK * 2;  // one 128 x 64 operand tile of a CTA, 16 KB
 template <int KIND>
 struct Cfg {
-  static constexpr bool FFN_ = KIND == FFN;
-  static constexpr int STAGES = FFN_ || KIND == GATED ? 4 : 6;
+  static constexpr int STAGES = KIND == FFN ? 4 : (KIND == QKNORM ? 6 : 5);
   // FFN: xm, dY (16 KB each), gate or up rows of Wgu (16 KB), 64 columns of Wd (8 KB)
-  static constexpr int STAGE = FFN_ ? 3 * OPERAND + OPERAND / 2 : 2 * OPERAND;
-  static constexpr int ACCS = FFN_ ? 1 : 2;  // TMEM accumulators: 256 + 128 columns, or 2 x 256
+  static constexpr int STAGE = KIND == FFN ? 3 * OPERAND + OPERAND / 2 : 2 * OPERAND;
+  static constexpr int ACCS = KIND == FFN ? 1 : 2;  // TMEM accumulators: 256 + 128 columns, or 2 x 256
   // Warp 0 TMA, warp 1 MMA, then EW epilogue warps: EW / 4 of each TMEM lane
   // quarter, sharing the tile's columns.  Sixteen hide the latency of the
   // TMEM and global accesses of one tile; QKNORM needs a head's 128 columns in
   // one warp and has eight.
   static constexpr int EW = KIND == QKNORM ? 8 : 16;
-  // GATED: one more warp loads the tile of W that the gate's gradient needs
-  static constexpr int THREADS = (2 + EW + (KIND == GATED ? 1 : 0)) * 32;
-  static constexpr int WTILE = KIND == GATED ? 4 * OPERAND : 0;  // 128 rows x 256 columns
+  // PRODUCTS: one more warp loads the tile of W that a gate's gradient needs.
+  // (Five stages beside its 64 KB: 2-4% faster than four for the gated
+  // product, and as fast as six for the others.)
+  static constexpr int THREADS = (2 + EW + (KIND == PRODUCTS ? 1 : 0)) * 32;
+  static constexpr int WTILE = KIND == PRODUCTS ? 4 * OPERAND : 0;  // 128 rows x 256 columns
   static constexpr int MISC = 768;
   static constexpr int NORM = KIND == QKNORM ? 8 * 2 * 128 * 4 : 0;  // [epilogue warp][q, k][128]
   static constexpr int BYTES = STAGES * STAGE + WTILE + 1024 + MISC + NORM;
@@ -128,18 +143,30 @@ __device__ __forceinline__ void store8w(uint32_t* dst, long ld, int m, int M, co
 __device__ __forceinline__ void store16(bf16* dst, long ld, int m, int M, const uint32_t* w) {
   store8w(reinterpret_cast<uint32_t*>(dst), ld / 2, m, M, w);
 }
-// the warp's columns [n0, n0 + COLS) of one split's fp32 partial [M][N]
-template <int COLS>
-__device__ __forceinline__ void store_part(float* part, int N, int n0, int m, int M, const float* v) {
-#pragma unroll
-  for (int c = 0; c < COLS; c += 8)
-    if (n0 + c < N)
-      store8w(reinterpret_cast<uint32_t*>(part + (long)m * N + n0 + c), N, m, M, reinterpret_cast<const uint32_t*>(v + c));
-}
 template <int N>
 __device__ __forceinline__ void pack_row(const float* v, uint32_t* w) {
 #pragma unroll
   for (int i = 0; i < N; i += 2) w[i / 2] = pack_bf16x2(v[i], v[i + 1]);
+}
+// The warp's columns [n0, n0 + COLS) of the output as bf16, or of one split's
+// partial as fp32
+template <int COLS>
+__device__ __forceinline__ void store_tile(const Product& pr, int sp, int n0, int m, const float* v) {
+  const int M = pr.M, N = pr.N;
+  if (pr.splits > 1) {
+    uint32_t* dst = reinterpret_cast<uint32_t*>(pr.part + ((long)sp * M + m) * N + n0);
+#pragma unroll
+    for (int c = 0; c < COLS; c += 8)
+      if (n0 + c < N) store8w(dst + c, N, m, M, reinterpret_cast<const uint32_t*>(v + c));
+  } else {
+    bf16* dst = pr.out + (long)m * N + n0;
+#pragma unroll
+    for (int c = 0; c < COLS; c += 16) {
+      uint32_t w[8];
+      pack_row<16>(v + c, w);
+      if (n0 + c < N) store16(dst + c, N, m, M, w);
+    }
+  }
 }
 __device__ __forceinline__ void unpack8(const uint4& u, float* f) {
   const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&u);
@@ -180,10 +207,10 @@ __device__ __forceinline__ void unrotate32(const bf16* d, bool valid, const floa
 // s inv / 128.  Two passes over the row's four chunks; sum_t t xhat, the
 // gradient of w, goes to wacc[128] of this warp.
 template <typename Release>
-__device__ __forceinline__ void epi_qknorm(const Params& p, uint32_t tb, int m, int n, const float* freq,
+__device__ __forceinline__ void epi_qknorm(const Params& p, uint32_t tb, int m, int n, int I, const float* freq,
                                            const uint8_t* axis, float* wacc2, Release release) {
   const int lane = threadIdx.x & 31;
-  const int part = n / p.I, hd = (n % p.I) / 128;
+  const int part = n / I, hd = (n % I) / 128;
   const bool valid = m < p.rows;
   const bf16* d = (part == 0 ? p.dq : p.dk) + ((long)hd * p.L_pad + (valid ? m : 0)) * 128;
   const bf16* w = part == 0 ? p.qn_w : p.kn_w;
@@ -246,9 +273,9 @@ __device__ __forceinline__ void epi_qknorm(const Params& p, uint32_t tb, int m, 
     wacc[c * 32 + lane] += t[0];
   }
   release();
-  bf16* dst = p.out + (long)m * p.ldo + n;
+  bf16* dst = p.dqkv + (long)m * 3 * p.I + n;
 #pragma unroll
-  for (int c = 0; c < 8; ++c) store16(dst + c * 16, p.ldo, m, p.rows, out + c * 8);
+  for (int c = 0; c < 8; ++c) store16(dst + c * 16, 3L * p.I, m, p.rows, out + c * 8);
 }
 
 // h = SiLU(g) u, du = dh SiLU(g), dg = dh u sig(g) (1 + g (1 - sig(g))) for 32 of
@@ -290,14 +317,41 @@ __device__ __forceinline__ void epi_ffn(const Params& p, uint32_t tb, int m, int
   }
 }
 
+// A unit of work: split sp of tile (mt, nt) of product pr
+struct Unit {
+  int product, sp, mt, nt;
+};
+template <int KIND>
+__device__ __forceinline__ Unit unit_of(const Params& p, int u) {
+  Unit w;
+  w.product = 0;
+  if constexpr (KIND == PRODUCTS)
+    while (u >= p.pr[w.product].units) u -= p.pr[w.product++].units;
+  const Product& pr = p.pr[w.product];
+  const int tiles = pr.m_tiles * pr.n_tiles;
+  w.sp = u / tiles;
+  tile_coords(u - w.sp * tiles, pr.m_tiles, pr.n_tiles, pr.group_m, w.mt, w.nt);
+  return w;
+}
+// k blocks [lo, hi) of segment sg in split sp, the segments' blocks counted one
+// after another
+__device__ __forceinline__ void seg_range(const Product& pr, int sp, int sg, int& lo, int& hi) {
+  int total = pr.kb[0], before = 0;
+  if (pr.segs > 1) {
+    total += pr.kb[1] + pr.kb[2];
+    before = sg == 0 ? 0 : (sg == 1 ? pr.kb[0] : pr.kb[0] + pr.kb[1]);
+  }
+  const int per = (total + pr.splits - 1) / pr.splits, n = pr.kb[sg];
+  lo = min(n, max(0, sp * per - before));
+  hi = max(lo, min(n, (sp + 1) * per - before));
+}
+
 template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 1)
     gemm_bwd_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   using C = Cfg<KIND>;
   constexpr int STAGES = C::STAGES, STAGE = C::STAGE, EW = C::EW;
   constexpr int COLS = 1024 / EW;  // output columns of an epilogue warp (FFN: 32)
-  constexpr bool A_MN = KIND == WGRAD || KIND == GATED;
-  constexpr bool B_MN = KIND != QKNORM && KIND != FFN;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -307,8 +361,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
-  uint64_t* w_full = drain + 1;   // GATED: W of the tile
-  uint64_t* w_empty = drain + 2;  // GATED: read by every epilogue warp of this CTA
+  uint64_t* w_full = drain + 1;   // PRODUCTS: W of the tile
+  uint64_t* w_empty = drain + 2;  // PRODUCTS: read by every epilogue warp of this CTA
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 3);
   float* freq = reinterpret_cast<float*>(tmem_slot + 4);
   uint8_t* axis = reinterpret_cast<uint8_t*>(freq + 64);
@@ -325,15 +379,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       mbar_init(&empty[s], 1);  // the leader's MMA commit, delivered to both CTAs
     }
     for (int a = 0; a < 2; ++a) {
-      mbar_init(&tfull[a], 1);    // the leader's commit, delivered to both CTAs
-      mbar_init(&tempty[a], 2 * EW);  // the epilogue warps of both CTAs (leader's copy used)
+      mbar_init(&tfull[a], 1);         // the leader's commit, delivered to both CTAs
+      mbar_init(&tempty[a], 2 * EW);   // the epilogue warps of both CTAs (leader's copy used)
     }
     mbar_init(drain, 1);
     mbar_init(w_full, 1);
     mbar_init(w_empty, EW);
     fence_mbar_init();
-    tma_prefetch_desc(&maps.a[0]);
-    tma_prefetch_desc(&maps.b[0]);
+    for (int i = 0; i < p.n_maps; ++i) tma_prefetch_desc(&maps.m[i]);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -359,25 +412,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
   const uint32_t tmem_base = *tmem_slot;
   chain_wait();
 
-  const int num_tiles = p.m_tiles * p.n_tiles;
-  const int num_units = num_tiles * p.splits;
-  constexpr int SEGS = KIND == GATED ? 3 : 1;
-  auto seg_kb = [&](int sg) {
-    return (KIND == WGRAD || KIND == GATED) ? (p.seg_rows[sg] + BK - 1) / BK : p.K / BK;
-  };
-  int kb_total = 0;
-  for (int sg = 0; sg < SEGS; ++sg) kb_total += seg_kb(sg);
-  const int kb_split = (kb_total + p.splits - 1) / p.splits;
-  // k blocks [lo, hi) of segment sg in split sp, the segments' blocks counted
-  // one after another
-  auto seg_range = [&](int sp, int sg, int& lo, int& hi) {
-    int before = 0;
-    for (int i = 0; i < sg; ++i) before += seg_kb(i);
-    const int n = seg_kb(sg);
-    lo = min(n, max(0, sp * kb_split - before));
-    hi = max(lo, min(n, (sp + 1) * kb_split - before));
-  };
-
   if (warp == 0) {
     if (lane == 0) {
       const uint32_t leader_full0 = mapa_shared(smem_u32(&full[0]), 0);
@@ -385,40 +419,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       uint32_t phase = 0;
       long long issued = 0;
       bool ok = true;
-      for (int u = pair; u < num_units && ok; u += n_pairs) {
-        int mt, nt;
-        const int sp = u / num_tiles;
-        tile_coords(u - sp * num_tiles, p.m_tiles, p.n_tiles, p.group_m, mt, nt);
-        const int a0 = mt * 256 + (int)rank * 128;  // this CTA's A rows (or MN-major columns)
-        const int b0 = nt * (KIND == FFN ? 128 : 256) + (int)rank * (KIND == FFN ? p.F : 128);
-        for (int sg = 0; sg < SEGS && ok; ++sg) {
+      for (int u = pair; u < p.units && ok; u += n_pairs) {
+        // One thread feeds the tile: everything its loop needs is in registers
+        // before it (a parameter indexed by the product costs the whole kernel
+        // 7% when it is read again for every load).
+        const Unit w = unit_of<KIND>(p, u);
+        const Product& pr = p.pr[w.product];  // 0 but for PRODUCTS
+        const int a0 = w.mt * 256 + (int)rank * 128;  // this CTA's A rows (or MN-major columns)
+        const int b0 = w.nt * (KIND == FFN ? 128 : 256) + (int)rank * (KIND == FFN ? p.F : 128);
+        const int d0 = w.nt * 128 + (int)rank * 64;
+        const int segs = pr.segs, map0 = pr.map0;
+        const bool a_mn = KIND == PRODUCTS && pr.a_mn;
+        for (int sg = 0; sg < segs && ok; ++sg) {
+          const CUtensorMap* ma = &maps.m[map0 + sg];
+          const CUtensorMap* mb = &maps.m[map0 + segs + sg];
           int lo, hi;
-          seg_range(sp, sg, lo, hi);
-          for (int kb = lo; kb < hi; ++kb) {
-            if (!mbar_wait(&empty[stage], phase ^ 1)) { ok = false; break; }
-            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * STAGE);
-            const uint32_t fb = leader_full0 + stage * 8;
-            uint8_t* sA = smem + stage * STAGE;
-            uint8_t* sB = sA + OPERAND;
-            if constexpr (A_MN) {
-              tma_load_2d_pair(sA, &maps.a[sg], fb, a0, kb * BK);
-              tma_load_2d_pair(sA + OPERAND / 2, &maps.a[sg], fb, a0 + 64, kb * BK);
-            } else {
-              tma_load_2d_pair(sA, &maps.a[0], fb, kb * BK, a0);
+          seg_range(pr, w.sp, sg, lo, hi);
+          auto feed = [&](auto a_tag) {
+            constexpr bool A_MN = decltype(a_tag)::value;
+            for (int kb = lo; kb < hi; ++kb) {
+              if (!mbar_wait(&empty[stage], phase ^ 1)) { ok = false; break; }
+              if (leader) mbar_arrive_expect_tx(&full[stage], 2 * STAGE);
+              const uint32_t fb = leader_full0 + stage * 8;
+              uint8_t* sA = smem + stage * STAGE;
+              uint8_t* sB = sA + OPERAND;
+              if constexpr (A_MN) {
+                tma_load_2d_pair(sA, ma, fb, a0, kb * BK);
+                tma_load_2d_pair(sA + OPERAND / 2, ma, fb, a0 + 64, kb * BK);
+              } else {
+                tma_load_2d_pair(sA, ma, fb, kb * BK, a0);
+              }
+              if constexpr (KIND == PRODUCTS) {
+                tma_load_2d_pair(sB, mb, fb, b0, kb * BK);
+                tma_load_2d_pair(sB + OPERAND / 2, mb, fb, b0 + 64, kb * BK);
+              } else {
+                tma_load_2d_pair(sB, mb, fb, kb * BK, b0);
+              }
+              if constexpr (KIND == FFN) {
+                tma_load_2d_pair(sA + 2 * OPERAND, &maps.m[2], fb, kb * BK, a0);
+                tma_load_2d_pair(sA + 3 * OPERAND, &maps.m[3], fb, d0, kb * BK);
+              }
+              ++issued;
+              if (++stage == STAGES) { stage = 0; phase ^= 1; }
             }
-            if constexpr (B_MN) {
-              tma_load_2d_pair(sB, &maps.b[sg], fb, b0, kb * BK);
-              tma_load_2d_pair(sB + OPERAND / 2, &maps.b[sg], fb, b0 + 64, kb * BK);
-            } else {
-              tma_load_2d_pair(sB, &maps.b[0], fb, kb * BK, b0);
-            }
-            if constexpr (KIND == FFN) {
-              tma_load_2d_pair(sA + 2 * OPERAND, &maps.a[1], fb, kb * BK, a0);
-              tma_load_2d_pair(sA + 3 * OPERAND, &maps.b[1], fb, nt * 128 + (int)rank * 64, kb * BK);
-            }
-            ++issued;
-            if (++stage == STAGES) { stage = 0; phase ^= 1; }
-          }
+          };
+          if (a_mn)
+            feed(std::true_type{});
+          else
+            feed(std::false_type{});
         }
       }
       // the leader's full barriers count both CTAs' bytes: the leader waits
@@ -427,30 +475,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
     }
   } else if (warp == 1) {
     if (leader) {
-      constexpr uint32_t idesc = idesc_bf16_f32(256, 256, B_MN) | (A_MN ? 1u << 15 : 0u);
-      constexpr uint32_t idesc_dh = idesc_bf16_f32(256, 128, true);
       // MN-major operands: 64-column blocks 8 KB apart, 8-row groups 1 KB
       // apart, 16 rows (2 KB) per MMA; K-major: 32 bytes per MMA
-      const uint64_t a_desc0 = sdesc_sw128(smem_u32(smem), A_MN ? OPERAND / 2 : 16, 1024);
+      constexpr bool B_MN = KIND == PRODUCTS;
       const uint64_t b_desc0 = sdesc_sw128(smem_u32(smem + OPERAND), B_MN ? OPERAND / 2 : 16, 1024);
       const uint64_t a2_desc0 = sdesc_sw128(smem_u32(smem + 2 * OPERAND), 16, 1024);
       const uint64_t b2_desc0 = sdesc_sw128(smem_u32(smem + 3 * OPERAND), OPERAND / 2, 1024);
-      constexpr uint64_t A_STEP = A_MN ? 128 : 2, B_STEP = B_MN ? 128 : 2;
+      constexpr uint32_t idesc_dh = idesc_bf16_f32(256, 128, true);
+      constexpr uint64_t B_STEP = B_MN ? 128 : 2;
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
-      for (int u = pair; u < num_units && ok; u += n_pairs) {
-        for (int sg = 0; sg < SEGS && ok; ++sg) {
+      for (int u = pair; u < p.units && ok; u += n_pairs) {
+        const Unit w = unit_of<KIND>(p, u);
+        const Product& pr = p.pr[w.product];
+        // the MMAs' descriptors are constants but for the start address: one
+        // loop for each majorness of A
+        auto contract = [&](auto a_tag, int sg) {
+          constexpr bool A_MN = decltype(a_tag)::value;
+          constexpr uint32_t idesc = idesc_bf16_f32(256, 256, B_MN) | (A_MN ? 1u << 15 : 0u);
+          constexpr uint64_t A_STEP = A_MN ? 128 : 2;
+          const uint64_t a_desc0 = sdesc_sw128(smem_u32(smem), A_MN ? OPERAND / 2 : 16, 1024);
           int lo, hi;
-          seg_range(u / num_tiles, sg, lo, hi);
-          if (lo == hi) continue;
-          if (!mbar_wait_warp(&tempty[acc], acc_phase ^ 1)) { ok = false; break; }
+          seg_range(pr, w.sp, sg, lo, hi);
+          if (lo == hi) return true;
+          if (!mbar_wait_warp(&tempty[acc], acc_phase ^ 1)) return false;
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + (uint32_t)(acc * 256);
           for (int kb = lo; kb < hi; ++kb) {
-            if (!mbar_wait_warp(&full[stage], phase)) { ok = false; break; }
+            if (!mbar_wait_warp(&full[stage], phase)) return false;
             tc_fence_after();
             const uint64_t off = (uint64_t)((stage * STAGE) >> 4);
 #pragma unroll
@@ -468,21 +523,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
           }
           umma_commit_pair(&tfull[acc]);
           if (++acc == C::ACCS) { acc = 0; acc_phase ^= 1; }
+          return true;
+        };
+        for (int sg = 0; sg < pr.segs && ok; ++sg) {
+          if (KIND == PRODUCTS && pr.a_mn)
+            ok = contract(std::true_type{}, sg);
+          else
+            ok = contract(std::false_type{}, sg);
         }
       }
       umma_commit_pair(drain);
       mbar_wait(drain, 0);
     }
-  } else if (warp >= 2 + EW) {  // GATED: the tiles of W
+  } else if (warp >= 2 + EW) {  // PRODUCTS: the gated product's tiles of W
     if (lane == 0 && p.gate_grad) {
       int n = 0;
-      for (int u = pair; u < num_units; u += n_pairs, ++n) {
-        int mt, nt;
-        tile_coords(u % num_tiles, p.m_tiles, p.n_tiles, p.group_m, mt, nt);
+      for (int u = pair; u < p.units; u += n_pairs) {
+        const Unit w = unit_of<KIND>(p, u);
+        const Product& pr = p.pr[w.product];
+        if (!pr.gated) continue;
         if (!mbar_wait(w_empty, (n & 1) ^ 1)) break;
         mbar_arrive_expect_tx(w_full, C::WTILE);
         for (int c = 0; c < 4; ++c)
-          tma_load_2d(sW + c * OPERAND, &maps.w, w_full, nt * 256 + c * 64, mt * 256 + (int)rank * 128);
+          tma_load_2d(sW + c * OPERAND, &maps.m[pr.map0 + 6], w_full, w.nt * 256 + c * 64,
+                      w.mt * 256 + (int)rank * 128);
+        ++n;
       }
       if (n > 0) mbar_wait(w_full, (n - 1) & 1);
     }
@@ -506,38 +571,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       if (++acc == C::ACCS) { acc = 0; acc_phase ^= 1; }
     };
     const uint32_t lane_off = (uint32_t)(q * 32) << 16;
-    int n_tile = 0;
-    for (int u = pair; u < num_units; u += n_pairs) {
-      int mt, nt;
-      const int sp = u / num_tiles;
-      tile_coords(u - sp * num_tiles, p.m_tiles, p.n_tiles, p.group_m, mt, nt);
-      float* part = p.part + (long)sp * p.M * p.N;
-      const int m = mt * 256 + (int)rank * 128 + row_in_tile;
-      const int n0 = nt * 256 + sub * COLS;
-      if constexpr (KIND == GATED) {
+    int n_w = 0;
+    for (int u = pair; u < p.units; u += n_pairs) {
+      const Unit w = unit_of<KIND>(p, u);
+      const Product& pr = p.pr[w.product];
+      const int m = w.mt * 256 + (int)rank * 128 + row_in_tile;
+      const int n0 = w.nt * 256 + sub * COLS;
+      if constexpr (KIND == FFN) {
+        if (!wait_full()) break;
+        epi_ffn(p, tmem_base + lane_off + (uint32_t)(acc * 256), m, w.nt, sub, release);
+      } else if constexpr (KIND == QKNORM) {
+        if (!wait_full()) break;
+        epi_qknorm(p, tmem_base + lane_off + (uint32_t)(acc * 256 + sub * COLS), m, n0, pr.N / 2, freq, axis,
+                   wacc + (warp - 2) * 256, release);
+      } else if (pr.gated) {
         // the warp's 64 output columns of this row stay in registers while the
         // modalities' accumulators come by; W's 64 columns (one swizzled box)
         // are in shared memory
         float sum[COLS];
 #pragma unroll
         for (int j = 0; j < COLS; ++j) sum[j] = 0.f;
-        const bool in = m < p.M;
+        const bool in = m < pr.M;
         const uint8_t* wrow = sW + sub * OPERAND + row_in_tile * 128;
         if (p.gate_grad) {
-          ok = mbar_wait_warp(w_full, n_tile & 1);
+          ok = mbar_wait_warp(w_full, n_w & 1);
           if (!ok) break;
         }
 #pragma unroll 1
         for (int sg = 0; sg < 3; ++sg) {
-          if (p.seg_rows[sg] == 0) continue;
-          float* gp = p.gate_part + ((long)(sg * p.splits + sp) * 4 * p.n_tiles + nt * 4 + sub) * p.M + m;
+          if (pr.kb[sg] == 0) continue;
+          float* gp = p.gate_part + ((long)(sg * pr.splits + w.sp) * 4 * pr.n_tiles + w.nt * 4 + sub) * pr.M + m;
           int lo, hi;
-          seg_range(sp, sg, lo, hi);
+          seg_range(pr, w.sp, sg, lo, hi);
           if (lo == hi) {  // none of this modality in this split
             if (p.gate_grad && in) *gp = 0.f;
             continue;
           }
-          const float gate = in ? __ldg(p.mod + (long)(sg * 6 + p.gate_slot) * p.D + m) : 0.f;
+          const float gate = in ? __ldg(p.mod + (long)(sg * 6 + p.gate_slot) * pr.M + m) : 0.f;
           if (!wait_full()) break;
           const uint32_t tb = tmem_base + lane_off + (uint32_t)(acc * 256 + sub * COLS);
           float dot = 0.f;
@@ -563,57 +633,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         }
         if (!ok) break;
         if (p.gate_grad) {
+          ++n_w;
           __syncwarp();
           if (lane == 0) mbar_arrive(w_empty);
         }
-        if (p.out != nullptr && p.splits > 1) {
-          store_part<COLS>(part, p.N, n0, m, p.M, sum);
-        } else if (p.out != nullptr) {
-#pragma unroll
-          for (int c = 0; c < COLS; c += 16) {
-            uint32_t w[8];
-            pack_row<16>(sum + c, w);
-            if (n0 + c < p.N) store16(p.out + (long)m * p.ldo + n0 + c, p.ldo, m, p.M, w);
-          }
-        }
+        if (pr.out != nullptr) store_tile<COLS>(pr, w.sp, n0, m, sum);
       } else {
         int lo, hi;
-        seg_range(sp, 0, lo, hi);
-        if (lo < hi && !wait_full()) break;
-        const uint32_t tb = tmem_base + lane_off + (uint32_t)(acc * 256);
-        // the accumulator is handed back before the tile's stores
-        if constexpr (KIND == FFN) {
-          epi_ffn(p, tb, m, nt, sub, release);
-        } else if constexpr (KIND == QKNORM) {
-          epi_qknorm(p, tb + sub * COLS, m, n0, freq, axis, wacc + (warp - 2) * 256, release);
-        } else if (p.splits > 1) {
-          float v[COLS];
-          if (lo < hi) {
+        seg_range(pr, w.sp, 0, lo, hi);
+        float v[COLS];
+        if (lo < hi) {
+          if (!wait_full()) break;
+          const uint32_t tb = tmem_base + lane_off + (uint32_t)(acc * 256 + sub * COLS);
 #pragma unroll
-            for (int c = 0; c < COLS; c += 32) ld_chunk(tb + sub * COLS + c, v + c);
-            tmem_wait_ld();
-            release();
-          } else {
-#pragma unroll
-            for (int c = 0; c < COLS; ++c) v[c] = 0.f;
-          }
-          store_part<COLS>(part, p.N, n0, m, p.M, v);
+          for (int c = 0; c < COLS; c += 32) ld_chunk(tb + c, v + c);
+          tmem_wait_ld();
+          release();  // before the stores
         } else {
-          uint32_t w[COLS / 2];
 #pragma unroll
-          for (int c = 0; c < COLS; c += 32) {
-            float v[32];
-            ld_chunk(tb + sub * COLS + c, v);
-            tmem_wait_ld();
-            pack_row<32>(v, w + c / 2);
-          }
-          release();
-#pragma unroll
-          for (int c = 0; c < COLS; c += 16)
-            if (n0 + c < p.N) store16(p.out + (long)m * p.ldo + n0 + c, p.ldo, m, p.M, w + c / 2);
+          for (int c = 0; c < COLS; ++c) v[c] = 0.f;
         }
+        store_tile<COLS>(pr, w.sp, n0, m, v);
       }
-      ++n_tile;
     }
   }
 
@@ -641,9 +682,9 @@ int max_cta_pairs() {
 
 // Splitting the contraction of a product with few output tiles.  In units of
 // one k block's MMAs (about 0.3 us): the longest pair's blocks, and for more
-// than one split a kernel (4 us) and the partials through memory.  Measured
-// at 5,376 x 28,672 over 512 rows (42 tiles for 74 pairs): see the case in the
-// launchers below.
+// than one split a kernel (4 us) and the partials through memory.  Measured:
+// 512 rows of 28,672 x 5,376 (42 tiles for 74 pairs) 212 -> 148 us in three
+// splits; 320 x 1,792 over 32,160 rows (14 tiles) 224 -> 59 us in five.
 constexpr size_t SPLIT_BYTES = 48u << 20;  // of the partials, at most
 int plan_splits(int M, int N, int num_kb) {
   const int tiles = (M + 255) / 256 * ((N + 255) / 256), pairs = max_cta_pairs();
@@ -662,31 +703,7 @@ int plan_splits(int M, int N, int num_kb) {
 }
 size_t split_bytes(int M, int N, int num_kb) {
   const int s = plan_splits(M, N, num_kb);
-  return s > 1 ? (size_t)s * M * N * 4 : 0;
-}
-
-template <int KIND>
-cudaError_t launch(const Maps& maps, Params p, cudaStream_t stream) {
-  static unsigned long long attr_done = 0;
-  const void* fn = reinterpret_cast<const void*>(gemm_bwd_kernel<KIND>);
-  cudaError_t e = ensure_smem_attr(fn, Cfg<KIND>::BYTES, &attr_done);
-  if (e != cudaSuccess) return e;
-  p.m_tiles = (p.M + 255) / 256;
-  p.n_tiles = (p.N + (KIND == FFN ? 127 : 255)) / (KIND == FFN ? 128 : 256);
-  // bands of eight row tiles: a wave of 74 tiles is then about 8 x 9, whose
-  // operands (17 panels) are the fewest a wave can read
-  p.group_m = p.m_tiles < 8 ? p.m_tiles : 8;
-  if (p.splits < 1) p.splits = 1;
-  const int units = p.m_tiles * p.n_tiles * p.splits;
-  const int max_pairs = max_cta_pairs();
-  const int pairs = units < max_pairs ? units : max_pairs;
-  return launch_chained(gemm_bwd_kernel<KIND>, dim3(2 * pairs), Cfg<KIND>::THREADS, Cfg<KIND>::BYTES, stream, maps, p);
-}
-
-// the sum of a split product's partials
-cudaError_t finish(const Params& p, cudaStream_t stream) {
-  static const int none[3] = {0, 0, 0};
-  return launch_finish_gated(nullptr, 0, none, 0, 0, nullptr, p.part, p.splits, (long)p.M * p.N, p.out, stream);
+  return s > 1 ? ((size_t)s * M * N * 4 + 255) / 256 * 256 : 0;
 }
 
 // K-major operand: rows x cols, 128-row boxes; MN-major: 64-row boxes
@@ -697,92 +714,128 @@ bool map_mn(CUtensorMap* m, const void* base, long rows, long cols, long ld) {
   return make_tmap_bf16(m, base, rows, cols, ld, 64);
 }
 
+void set_tiles(Product& pr, int M, int N, int n_step) {
+  pr.M = M;
+  pr.N = N;
+  pr.m_tiles = (M + 255) / 256;
+  pr.n_tiles = (N + n_step - 1) / n_step;
+  // bands of eight row tiles: a wave of 74 tiles is then about 8 x 9, whose
+  // operands (17 panels) are the fewest a wave can read (measured at 32,160
+  // tokens: four or twelve rows 3-8% slower)
+  pr.group_m = pr.m_tiles < 8 ? pr.m_tiles : 8;
+}
+
+template <int KIND>
+cudaError_t launch(const Maps& maps, Params& p, cudaStream_t stream) {
+  static unsigned long long attr_done = 0;
+  const void* fn = reinterpret_cast<const void*>(gemm_bwd_kernel<KIND>);
+  cudaError_t e = ensure_smem_attr(fn, Cfg<KIND>::BYTES, &attr_done);
+  if (e != cudaSuccess) return e;
+  p.units = 0;
+  for (int i = 0; i < p.n_products; ++i) {
+    Product& pr = p.pr[i];
+    pr.units = pr.m_tiles * pr.n_tiles * pr.splits;
+    p.units += pr.units;
+  }
+  const int max_pairs = max_cta_pairs();
+  const int pairs = p.units < max_pairs ? p.units : max_pairs;
+  return launch_chained(gemm_bwd_kernel<KIND>, dim3(2 * pairs), Cfg<KIND>::THREADS, Cfg<KIND>::BYTES, stream, maps, p);
+}
+
 }  // namespace gemm_bwd
-
-// out [out_rows][N] = A [rows][K] B [K][N] for token rows (rows past `rows`: 0)
-// (part: split_bytes(out_rows, N, K / 64) of scratch)
-cudaError_t launch_dgrad(const bf16* A, const bf16* B, int rows, int out_rows, int N, int K, bf16* out, float* part,
-                         cudaStream_t stream) {
-  using namespace gemm_bwd;
-  Maps maps;
-  Params p;
-  memset(&maps, 0, sizeof(maps));
-  memset(&p, 0, sizeof(p));
-  if (!map_k(&maps.a[0], A, rows, K, K) || !map_mn(&maps.b[0], B, K, N, N)) return cudaErrorInvalidValue;
-  p.M = out_rows;
-  p.N = N;
-  p.K = K;
-  p.rows = rows;
-  p.out = out;
-  p.ldo = N;
-  p.splits = plan_splits(out_rows, N, K / gemm_bwd::BK);
-  p.part = part;
-  const cudaError_t e = launch<DGRAD>(maps, p, stream);
-  return e != cudaSuccess ? e : finish(p, stream);
-}
-
-// out [M][N] = A [rows][M]^T B [rows][N] (part: split_bytes(M, N, L_pad / 64))
-cudaError_t launch_wgrad(const bf16* A, const bf16* B, int rows, int L_pad, int M, int N, bf16* out, float* part,
-                         cudaStream_t stream) {
-  using namespace gemm_bwd;
-  Maps maps;
-  Params p;
-  memset(&maps, 0, sizeof(maps));
-  memset(&p, 0, sizeof(p));
-  if (!map_mn(&maps.a[0], A, rows, M, M) || !map_mn(&maps.b[0], B, rows, N, N)) return cudaErrorInvalidValue;
-  p.M = M;
-  p.N = N;
-  p.rows = p.seg_rows[0] = rows;
-  p.out = out;
-  p.ldo = N;
-  p.splits = plan_splits(M, N, L_pad / gemm_bwd::BK);
-  p.part = part;
-  const cudaError_t e = launch<WGRAD>(maps, p, stream);
-  return e != cudaSuccess ? e : finish(p, stream);
-}
 
 // Partials of the gate's gradient for each modality
 int gate_parts(int M, int N, int L_pad) {
   return 4 * ((N + 255) / 256) * gemm_bwd::plan_splits(M, N, L_pad / gemm_bwd::BK);
 }
 
+// The products that end a backward call: added one by one, then launched
+// together.  Partials of split products take their parts of `split` one after
+// another (split_bytes each, 256-byte aligned).
+struct Products {
+  gemm_bwd::Maps maps;
+  gemm_bwd::Params p;
+  FinishArgs fin;
+  uint8_t* split;
+  int n_maps = 0;
+  bool good = true;
 
-// dW [M][N] = sum_m gate_m (.) A_m^T B_m over the modality ranges (out; null: no
-// weight gradient), and the gate's gradient into its slot of dmod (null: none)
-// by way of gate_part [3][gate_parts][M]; W: the weight behind the gate
-// (part: split_bytes(M, N, L_pad / 64))
-cudaError_t launch_wgrad_gated(const bf16* A, const bf16* B, const int* start, const int* count, int L_pad, int M, int N,
-                               const float* mod, int gate_slot, const bf16* W, bf16* out, bf16* dmod, float* gate_part,
-                               float* part, cudaStream_t stream) {
-  using namespace gemm_bwd;
-  Maps maps;
-  Params p;
-  memset(&maps, 0, sizeof(maps));
-  memset(&p, 0, sizeof(p));
-  for (int m = 0; m < 3; ++m) {
-    p.seg_rows[m] = count[m];
-    if (count[m] == 0) continue;
-    if (!map_mn(&maps.a[m], A + (long)start[m] * M, count[m], M, M) ||
-        !map_mn(&maps.b[m], B + (long)start[m] * N, count[m], N, N))
-      return cudaErrorInvalidValue;
+  explicit Products(float* split_ws) : split(reinterpret_cast<uint8_t*>(split_ws)) {
+    memset(&maps, 0, sizeof(maps));
+    memset(&p, 0, sizeof(p));
+    memset(&fin, 0, sizeof(fin));
   }
-  p.M = M;
-  p.N = N;
-  p.out = out;
-  p.ldo = N;
-  p.mod = mod;
-  p.gate_slot = gate_slot;
-  p.D = M;
-  p.gate_grad = dmod != nullptr;
-  if (p.gate_grad && !map_k(&maps.w, W, M, N, N)) return cudaErrorInvalidValue;
-  p.gate_part = gate_part;
-  p.splits = plan_splits(M, N, L_pad / gemm_bwd::BK);
-  p.part = part;
-  const cudaError_t e = launch<GATED>(maps, p, stream);
-  if (e != cudaSuccess) return e;
-  return launch_finish_gated(gate_part, gate_parts(M, N, L_pad), count, M, gate_slot, dmod, part, p.splits, (long)M * N,
-                             out, stream);
-}
+  gemm_bwd::Product& add(int M, int N, int segs, int splits, bf16* out) {
+    gemm_bwd::Product& pr = p.pr[p.n_products++];
+    pr.map0 = n_maps;
+    pr.segs = segs;
+    gemm_bwd::set_tiles(pr, M, N, 256);
+    pr.splits = splits;
+    pr.out = out;
+    if (splits > 1) {
+      pr.part = reinterpret_cast<float*>(split);
+      split += ((size_t)splits * M * N * 4 + 255) / 256 * 256;
+      if (out != nullptr) fin.sum[fin.n_sums++] = {pr.part, out, (long)M * N, splits};
+    }
+    return pr;
+  }
+  // out [out_rows][N] = A [rows][K] B [K][N] (token rows past `rows`: 0)
+  void input_gradient(const bf16* A, const bf16* B, int rows, int out_rows, int N, int K, bf16* out) {
+    using namespace gemm_bwd;
+    Product& pr = add(out_rows, N, 1, plan_splits(out_rows, N, K / gemm_bwd::BK), out);
+    pr.kb[0] = K / gemm_bwd::BK;
+    good = good && map_k(&maps.m[n_maps], A, rows, K, K) && map_mn(&maps.m[n_maps + 1], B, K, N, N);
+    n_maps += 2;
+  }
+  // out [M][N] = A [rows][M]^T B [rows][N]
+  void weight_gradient(const bf16* A, const bf16* B, int rows, int L_pad, int M, int N, bf16* out) {
+    using namespace gemm_bwd;
+    Product& pr = add(M, N, 1, plan_splits(M, N, L_pad / gemm_bwd::BK), out);
+    pr.a_mn = 1;
+    pr.kb[0] = (rows + gemm_bwd::BK - 1) / gemm_bwd::BK;
+    good = good && map_mn(&maps.m[n_maps], A, rows, M, M) && map_mn(&maps.m[n_maps + 1], B, rows, N, N);
+    n_maps += 2;
+  }
+  // dW [M][N] = sum_m gate_m (.) A_m^T B_m over the modality ranges (null: not
+  // wanted), and the gate's gradient into its slot of dmod (null: not wanted)
+  // by way of gate_part [3][gate_parts][M]; W: the weight behind the gate
+  void gated_weight_gradient(const bf16* A, const bf16* B, const int* start, const int* count, int L_pad, int M, int N,
+                             const float* mod, int slot, const bf16* W, bf16* dW, bf16* dmod, float* gate_part) {
+    using namespace gemm_bwd;
+    Product& pr = add(M, N, 3, plan_splits(M, N, L_pad / gemm_bwd::BK), dW);
+    pr.a_mn = pr.gated = 1;
+    for (int m = 0; m < 3; ++m) {
+      pr.kb[m] = (count[m] + gemm_bwd::BK - 1) / gemm_bwd::BK;
+      if (count[m] == 0) continue;
+      good = good && map_mn(&maps.m[n_maps + m], A + (long)start[m] * M, count[m], M, M) &&
+             map_mn(&maps.m[n_maps + 3 + m], B + (long)start[m] * N, count[m], N, N);
+    }
+    good = good && map_k(&maps.m[n_maps + 6], W, M, N, N);
+    n_maps += 7;
+    p.mod = mod;
+    p.gate_slot = slot;
+    p.gate_grad = dmod != nullptr;
+    p.gate_part = gate_part;
+    if (dmod != nullptr) {
+      const int n = gate_parts(M, N, L_pad);
+      for (int m = 0; m < 3; ++m) {
+        fin.reduce.begin[m] = m * n;
+        fin.reduce.end[m] = count[m] > 0 ? (m + 1) * n : m * n;  // no tokens: 0
+        fin.reduce.out[m] = dmod + (long)(m * 6 + slot) * M;
+      }
+      fin.n_reduce = 3;
+      fin.reduce_part = gate_part;
+      fin.reduce_stride = M;
+      fin.reduce_cols = M;
+    }
+  }
+  cudaError_t run(cudaStream_t stream) {
+    if (!good) return cudaErrorInvalidValue;
+    p.n_maps = n_maps;
+    const cudaError_t e = gemm_bwd::launch<gemm_bwd::PRODUCTS>(maps, p, stream);
+    return e != cudaSuccess ? e : launch_finish(fin, stream);
+  }
+};
 
 // h [rows][F] and dgu [rows][2F] from xm, dy [rows][D], Wgu [2F][D], Wd [D][F]
 cudaError_t launch_ffn_bwd(const bf16* xm, const bf16* dy, const bf16* Wgu, const bf16* Wd, int rows, int D, int F,
@@ -792,12 +845,15 @@ cudaError_t launch_ffn_bwd(const bf16* xm, const bf16* dy, const bf16* Wgu, cons
   Params p;
   memset(&maps, 0, sizeof(maps));
   memset(&p, 0, sizeof(p));
-  if (!map_k(&maps.a[0], xm, rows, D, D) || !map_k(&maps.a[1], dy, rows, D, D) || !map_k(&maps.b[0], Wgu, 2 * F, D, D) ||
-      !map_mn(&maps.b[1], Wd, D, F, F))
+  if (!map_k(&maps.m[0], xm, rows, D, D) || !map_k(&maps.m[1], Wgu, 2 * F, D, D) ||
+      !map_k(&maps.m[2], dy, rows, D, D) || !map_mn(&maps.m[3], Wd, D, F, F))
     return cudaErrorInvalidValue;
-  p.M = rows;
-  p.N = F;
-  p.K = D;
+  p.n_products = 1;
+  Product& pr = p.pr[0];
+  p.n_maps = 4;
+  set_tiles(pr, rows, F, 128);
+  pr.segs = pr.splits = 1;
+  pr.kb[0] = D / gemm_bwd::BK;
   p.rows = rows;
   p.F = F;
   p.h = h;
@@ -817,13 +873,15 @@ cudaError_t launch_qknorm_bwd(const bf16* xm, const bf16* Wqkv, const bf16* dq, 
   Params p;
   memset(&maps, 0, sizeof(maps));
   memset(&p, 0, sizeof(p));
-  if (!map_k(&maps.a[0], xm, rows, D, D) || !map_k(&maps.b[0], Wqkv, 2 * I, D, D)) return cudaErrorInvalidValue;
-  p.M = rows;
-  p.N = 2 * I;
-  p.K = D;
+  if (!map_k(&maps.m[0], xm, rows, D, D) || !map_k(&maps.m[1], Wqkv, 2 * I, D, D)) return cudaErrorInvalidValue;
+  p.n_products = 1;
+  Product& pr = p.pr[0];
+  p.n_maps = 2;
+  set_tiles(pr, rows, 2 * I, 256);
+  pr.segs = pr.splits = 1;
+  pr.kb[0] = D / gemm_bwd::BK;
   p.rows = rows;
-  p.out = dqkv;
-  p.ldo = 3L * I;
+  p.dqkv = dqkv;
   p.dq = dq;
   p.dk = dk;
   p.qn_w = qn_w;
@@ -837,8 +895,7 @@ cudaError_t launch_qknorm_bwd(const bf16* xm, const bf16* Wqkv, const bf16* dq, 
   p.theta = theta;
   p.eps_qk = eps;
   p.w_part = w_part;
-  const int tiles = (rows + 255) / 256 * ((2 * I + 255) / 256);
-  const int max_pairs = max_cta_pairs();
+  const int tiles = pr.m_tiles * pr.n_tiles, max_pairs = max_cta_pairs();
   *n_parts = 2 * (tiles < max_pairs ? tiles : max_pairs);
   return launch<QKNORM>(maps, p, stream);
 }

@@ -1,7 +1,5 @@
 // C ABI of the block's backward pass (declarations and contracts:
 // include/h3.h), included by h3_api.cu, whose checks it uses.
-#include <initializer_list>
-
 #include "backward.cu"
 #include "gemm_bwd.cu"
 #include "attention_bwd.cu"
@@ -23,28 +21,24 @@ struct Carve {
 
 struct GatedWs {  // h3_gated_residual_backward and the outer half of h3_ffn_swiglu_backward
   bf16 *plain, *gated;
-  float *gate_part, *split;  // split: partials of whichever product is being split
+  float *gate_part, *split;  // split: partials of the split products, one after another
 };
-size_t max_of(std::initializer_list<size_t> v) {
-  size_t m = 0;
-  for (size_t x : v) m = x > m ? x : m;
-  return m;
-}
 GatedWs carve_gated(Carve& c, const h3_dims* d, int L_pad, int K, size_t more_split) {
   using gemm_bwd::split_bytes;
   GatedWs w;
   w.plain = c.take<bf16>((size_t)L_pad * d->D);
   w.gated = c.take<bf16>((size_t)L_pad * d->D);
   w.gate_part = c.take<float>((size_t)3 * gate_parts(d->D, K, L_pad) * d->D);
-  w.split = c.take<float>(max_of({split_bytes(d->D, K, L_pad / 64), more_split}) / 4);
+  w.split = c.take<float>((split_bytes(d->D, K, L_pad / 64) + more_split) / 4);
   return w;
 }
 GatedWs carve_out(Carve& c, const h3_dims* d, int L_pad) {
   return carve_gated(c, d, L_pad, d->I, gemm_bwd::split_bytes(L_pad, d->I, d->D / 64));
 }
 GatedWs carve_ffn(Carve& c, const h3_dims* d, int L_pad) {
-  return carve_gated(c, d, L_pad, d->F, max_of({gemm_bwd::split_bytes(L_pad, d->D, 2 * d->F / 64),
-                                                gemm_bwd::split_bytes(2 * d->F, d->D, L_pad / 64)}));
+  using gemm_bwd::split_bytes;
+  return carve_gated(c, d, L_pad, d->F,
+                     split_bytes(L_pad, d->D, 2 * d->F / 64) + split_bytes(2 * d->F, d->D, L_pad / 64));
 }
 struct QkvWs {
   bf16* dqkv;
@@ -55,7 +49,7 @@ QkvWs carve_qkv(Carve& c, const h3_dims* d, int L_pad) {
   QkvWs w;
   w.dqkv = c.take<bf16>((size_t)L_pad * 3 * d->I);
   w.norm_part = c.take<float>((size_t)QKNORM_PARTS * 2 * 128);
-  w.split = c.take<float>(max_of({split_bytes(L_pad, d->D, 3 * d->I / 64), split_bytes(3 * d->I, d->D, L_pad / 64)}) / 4);
+  w.split = c.take<float>((split_bytes(L_pad, d->D, 3 * d->I / 64) + split_bytes(3 * d->I, d->D, L_pad / 64)) / 4);
   return w;
 }
 
@@ -72,16 +66,6 @@ int check_branch(int branch, const char* fn) {
 
 bf16* b16(h3_bf16* p) { return reinterpret_cast<bf16*>(p); }
 const bf16* b16(const h3_bf16* p) { return reinterpret_cast<const bf16*>(p); }
-
-// The weight's and the gate's gradient of y = gate (.) (B W^T) (either may be
-// NULL), from plain = bf16(dx) [L][D] and B [L][K]
-cudaError_t gated_weight_grads(const h3_dims* dims, const h3_ranges* r, const GatedWs& w, const bf16* B, int K,
-                               const h3_bf16* W, const float* mod, int slot, h3_bf16* dW, h3_bf16* dmod,
-                               cudaStream_t st) {
-  if (!dW && !dmod) return cudaSuccess;
-  return launch_wgrad_gated(w.plain, B, r->start, r->count, r->L_pad, dims->D, K, mod, slot, b16(W), b16(dW), b16(dmod),
-                            w.gate_part, w.split, st);
-}
 
 }  // namespace
 
@@ -157,12 +141,21 @@ int h3_qkv_qknorm_mrope_backward(const h3_dims* dims, const h3_ranges* ranges, c
   if (e != cudaSuccess) return cuda_fail(e, "h3_qkv_qknorm_mrope_backward: norm and RoPE");
   e = launch_dv_rows(b16(dv), dims->H, L, Lp, w.dqkv, st);
   if (e != cudaSuccess) return cuda_fail(e, "h3_qkv_qknorm_mrope_backward: dv");
-  e = launch_norm_weight_reduce(w.norm_part, n_parts, b16(dqn_w), b16(dkn_w), st);
-  if (e != cudaSuccess) return cuda_fail(e, "h3_qkv_qknorm_mrope_backward: norm weights");
-  e = launch_dgrad(w.dqkv, b16(Wqkv), L, Lp, D, 3 * I, b16(dxm), w.split, st);
-  if (e != cudaSuccess) return cuda_fail(e, "h3_qkv_qknorm_mrope_backward: dxm");
-  if (dWqkv) e = launch_wgrad(w.dqkv, b16(xm), L, Lp, 3 * I, D, b16(dWqkv), w.split, st);
-  if (e != cudaSuccess) return cuda_fail(e, "h3_qkv_qknorm_mrope_backward: dWqkv");
+  Products g(w.split);
+  g.input_gradient(w.dqkv, b16(Wqkv), L, Lp, D, 3 * I, b16(dxm));
+  if (dWqkv) g.weight_gradient(w.dqkv, b16(xm), L, Lp, 3 * I, D, b16(dWqkv));
+  if (dqn_w || dkn_w) {  // norm_part [n_parts][2][128]
+    g.fin.n_reduce = 2;
+    g.fin.reduce.end[0] = g.fin.reduce.end[1] = n_parts;
+    g.fin.reduce.out[0] = b16(dqn_w);
+    g.fin.reduce.out[1] = b16(dkn_w);
+    g.fin.reduce_part = w.norm_part;
+    g.fin.reduce_stride = 256;
+    g.fin.reduce_offset = 128;
+    g.fin.reduce_cols = 128;
+  }
+  e = g.run(st);
+  if (e != cudaSuccess) return cuda_fail(e, "h3_qkv_qknorm_mrope_backward: dxm, dWqkv");
   return ok();
 }
 
@@ -245,10 +238,13 @@ int h3_gated_residual_backward(const h3_dims* dims, const h3_ranges* ranges, con
   cudaError_t e = launch_gate_cast(dx, mod, slot, ranges->start, ranges->count, L, D, dWo || dmod ? w.plain : nullptr,
                                    w.gated, st);
   if (e != cudaSuccess) return cuda_fail(e, "h3_gated_residual_backward: gate");
-  e = launch_dgrad(w.gated, b16(Wo), L, ranges->L_pad, I, D, b16(d_o), w.split, st);
-  if (e != cudaSuccess) return cuda_fail(e, "h3_gated_residual_backward: do");
-  e = gated_weight_grads(dims, ranges, w, b16(o), I, Wo, mod, slot, dWo, dmod, st);
-  if (e != cudaSuccess) return cuda_fail(e, "h3_gated_residual_backward: dWo");
+  Products g(w.split);
+  g.input_gradient(w.gated, b16(Wo), L, ranges->L_pad, I, D, b16(d_o));
+  if (dWo || dmod)
+    g.gated_weight_gradient(w.plain, b16(o), ranges->start, ranges->count, ranges->L_pad, D, I, mod, slot, b16(Wo),
+                            b16(dWo), b16(dmod), w.gate_part);
+  e = g.run(st);
+  if (e != cudaSuccess) return cuda_fail(e, "h3_gated_residual_backward: do, dWo");
   return ok();
 }
 
@@ -279,12 +275,14 @@ int h3_ffn_swiglu_backward(const h3_dims* dims, const h3_ranges* ranges, const f
   if (e != cudaSuccess) return cuda_fail(e, "h3_ffn_swiglu_backward: gate");
   e = launch_ffn_bwd(b16(xm), w.gated, b16(Wgu), b16(Wd), L, D, F, h, dgu, st);
   if (e != cudaSuccess) return cuda_fail(e, "h3_ffn_swiglu_backward: hidden state");
-  e = launch_dgrad(dgu, b16(Wgu), L, Lp, D, 2 * F, b16(dxm), w.split, st);
-  if (e != cudaSuccess) return cuda_fail(e, "h3_ffn_swiglu_backward: dxm");
-  if (dWgu) e = launch_wgrad(dgu, b16(xm), L, Lp, 2 * F, D, b16(dWgu), w.split, st);
-  if (e != cudaSuccess) return cuda_fail(e, "h3_ffn_swiglu_backward: dWgu");
-  e = gated_weight_grads(dims, ranges, w, h, F, Wd, mod, slot, dWd, dmod, st);
-  if (e != cudaSuccess) return cuda_fail(e, "h3_ffn_swiglu_backward: dWd");
+  Products g(w.split);  // the longest contraction first
+  g.input_gradient(dgu, b16(Wgu), L, Lp, D, 2 * F, b16(dxm));
+  if (dWgu) g.weight_gradient(dgu, b16(xm), L, Lp, 2 * F, D, b16(dWgu));
+  if (dWd || dmod)
+    g.gated_weight_gradient(w.plain, h, ranges->start, ranges->count, Lp, D, F, mod, slot, b16(Wd), b16(dWd), b16(dmod),
+                            w.gate_part);
+  e = g.run(st);
+  if (e != cudaSuccess) return cuda_fail(e, "h3_ffn_swiglu_backward: dxm, dWgu, dWd");
   return ok();
 }
 
