@@ -27,19 +27,22 @@ constexpr int AB_STAGES = 4;
 constexpr int AB_SMEM = 216 * 1024;  // per SM, for the stages of its CTAs
 
 struct AdalnPlan {
-  int threads;   // one float4 column each, up to 512; wider rows take several
-  int per_sm;    // CTAs per SM: narrow rows need several to keep enough bytes in flight
+  int vpt;       // float4 columns of a thread
+  int threads;   // of a CTA, up to 512
+  int per_sm;    // CTAs per SM: one row's reductions hide behind another's arithmetic
   int stages;
   int ctas;      // partial rows, at most
 };
 static AdalnPlan adaln_plan(int D) {
   AdalnPlan p;
   const int nv = D / 4;
-  p.threads = nv >= AB_MAX_THREADS ? AB_MAX_THREADS : (nv + 31) / 32 * 32;
-  p.per_sm = AB_MAX_THREADS / p.threads;
+  p.vpt = (nv + AB_MAX_THREADS - 1) / AB_MAX_THREADS;
+  p.threads = ((nv + p.vpt - 1) / p.vpt + 31) / 32 * 32;
+  p.per_sm = 1024 / p.threads;
   if (p.per_sm > 8) p.per_sm = 8;
+  while (p.per_sm > 1 && AB_SMEM / p.per_sm < 20 * D) --p.per_sm;  // two stages at least: 20 D <= 160 KB
   const int fit = AB_SMEM / p.per_sm / (10 * D);
-  p.stages = fit < AB_STAGES ? fit : AB_STAGES;  // at least 2: 20 D <= 160 KB
+  p.stages = fit < AB_STAGES ? fit : AB_STAGES;
   p.ctas = 148 * p.per_sm;
   return p;
 }
@@ -72,15 +75,20 @@ __device__ __forceinline__ void block_sums(float* v, float* red) {
   }
 }
 
-__device__ __forceinline__ float4 unpack4(const uint2& g) {
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&g.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&g.y));
-  return make_float4(a.x, a.y, b.x, b.y);
+// a pair of bf16 as a packed pair of fp32
+__device__ __forceinline__ uint64_t f2_of_bf16(uint32_t w) {
+  return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float f2_sum(uint64_t a, uint64_t b) {
+  float x, y;
+  f2_unpack(f2_add(a, b), x, y);
+  return x + y;
 }
 
-// VPT: float4 columns per thread (D <= 4 VPT threads)
+// VPT: float4 columns per thread (D <= 4 VPT threads); arithmetic on packed
+// pairs of fp32
 template <int VPT>
-__global__ void __launch_bounds__(AB_MAX_THREADS) adaln_bwd_kernel(
+__global__ void __launch_bounds__(AB_MAX_THREADS, VPT <= 3 ? 2 : 1) adaln_bwd_kernel(
     const float* __restrict__ x, const float* __restrict__ mod, int branch, const bf16* __restrict__ dy,
     const float* dres, float* dx, RangeArgs rg, Chunks ch, int L, int L_pad, int D, float eps, int stages,
     float* __restrict__ part) {
@@ -118,81 +126,91 @@ __global__ void __launch_bounds__(AB_MAX_THREADS) adaln_bwd_kernel(
   if (threadIdx.x == 0)
     for (int i = 0; i < stages - 1 && i < n_rows; ++i) load_row(i);
   const float4* scale = reinterpret_cast<const float4*>(mod + (long)(m * 6 + 3 * branch + 1) * D);
-  float4 a_shift[VPT], a_scale[VPT], sc[VPT];
+  uint64_t a_shift[VPT][2], a_scale[VPT][2], sc[VPT][2];
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
     const int i = threadIdx.x + k * T;
-    a_shift[k] = a_scale[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    sc[k] = i < nv ? __ldg(scale + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-    sc[k] = make_float4(1.f + sc[k].x, 1.f + sc[k].y, 1.f + sc[k].z, 1.f + sc[k].w);
+    const float4 t = i < nv ? __ldg(scale + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    sc[k][0] = f2_pack(1.f + t.x, 1.f + t.y);
+    sc[k][1] = f2_pack(1.f + t.z, 1.f + t.w);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) a_shift[k][j] = a_scale[k][j] = 0ull;
   }
   bool ok = true;
   for (int r = 0; r < n_rows && ok; ++r) {
     const int st = r % stages;
-    const float4* xr = reinterpret_cast<const float4*>(smem_ab + st * stage_bytes);
-    const float4* rr = xr + nv;
+    const ulonglong2* xr = reinterpret_cast<const ulonglong2*>(smem_ab + st * stage_bytes);
+    const ulonglong2* rr = xr + nv;
     const uint2* yr = reinterpret_cast<const uint2*>(rr + nv);
     ok = mbar_wait(&full[st], (r / stages) & 1);
-    float4 v[VPT];
+    uint64_t v[VPT][2];
     float s1[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int i = threadIdx.x + k * T;
-      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < nv) v[k] = xr[i];
-      s1[0] += (v[k].x + v[k].y) + (v[k].z + v[k].w);
+      v[k][0] = v[k][1] = 0ull;
+      if (i < nv) {
+        const ulonglong2 t = xr[i];
+        v[k][0] = t.x;
+        v[k][1] = t.y;
+      }
+      s1[0] += f2_sum(v[k][0], v[k][1]);
     }
     block_sums<1>(s1, red[0]);
     // every thread has left row r - 1, whose stage takes row r + stages - 1
     if (threadIdx.x == 0 && r + stages - 1 < n_rows) load_row(r + stages - 1);
     const float mu = s1[0] / (float)D;  // divided as the forward call divides: a constant row has xhat = 0
-    float s3[3] = {0.f, 0.f, 0.f};      // sum (x - mu)^2, sum dh, sum dh (x - mu)
+    const uint64_t nmu = f2_pack(-mu, -mu);
+    uint64_t q[3] = {0ull, 0ull, 0ull};  // sum (x - mu)^2, sum dh, sum dh (x - mu)
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int i = threadIdx.x + k * T;
       if (i < nv) {
-        v[k] = make_float4(v[k].x - mu, v[k].y - mu, v[k].z - mu, v[k].w - mu);
-        const float4 g = unpack4(yr[i]);
-        const float4 h = make_float4(g.x * sc[k].x, g.y * sc[k].y, g.z * sc[k].z, g.w * sc[k].w);
-        s3[0] += (v[k].x * v[k].x + v[k].y * v[k].y) + (v[k].z * v[k].z + v[k].w * v[k].w);
-        s3[1] += (h.x + h.y) + (h.z + h.w);
-        s3[2] += (h.x * v[k].x + h.y * v[k].y) + (h.z * v[k].z + h.w * v[k].w);
+        const uint2 g = yr[i];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          v[k][j] = f2_add(v[k][j], nmu);
+          const uint64_t h = f2_mul(f2_of_bf16(j == 0 ? g.x : g.y), sc[k][j]);
+          q[0] = f2_fma(v[k][j], v[k][j], q[0]);
+          q[1] = f2_add(q[1], h);
+          q[2] = f2_fma(h, v[k][j], q[2]);
+        }
       }
     }
+    float s3[3] = {f2_sum(q[0], 0ull), f2_sum(q[1], 0ull), f2_sum(q[2], 0ull)};
     block_sums<3>(s3, red[1]);
     const float rstd = rsqrtf(s3[0] / (float)D + eps);
     const float mean_h = s3[1] / (float)D, mean_hx = s3[2] / (float)D * rstd;  // mean(dh), mean(dh xhat)
+    const uint64_t rs = f2_pack(rstd, rstd), nmh = f2_pack(-mean_h, -mean_h), nmx = f2_pack(-mean_hx, -mean_hx);
     float4* out = reinterpret_cast<float4*>(dx + (row0 + r) * D);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int i = threadIdx.x + k * T;
       if (i < nv) {
-        const float4 g = unpack4(yr[i]), res = rr[i];
-        const float4 xh = make_float4(v[k].x * rstd, v[k].y * rstd, v[k].z * rstd, v[k].w * rstd);
-        a_shift[k].x += g.x;
-        a_shift[k].y += g.y;
-        a_shift[k].z += g.z;
-        a_shift[k].w += g.w;
-        a_scale[k].x = fmaf(g.x, xh.x, a_scale[k].x);
-        a_scale[k].y = fmaf(g.y, xh.y, a_scale[k].y);
-        a_scale[k].z = fmaf(g.z, xh.z, a_scale[k].z);
-        a_scale[k].w = fmaf(g.w, xh.w, a_scale[k].w);
-        float4 o;
-        o.x = fmaf(rstd, g.x * sc[k].x - mean_h - xh.x * mean_hx, res.x);
-        o.y = fmaf(rstd, g.y * sc[k].y - mean_h - xh.y * mean_hx, res.y);
-        o.z = fmaf(rstd, g.z * sc[k].z - mean_h - xh.z * mean_hx, res.z);
-        o.w = fmaf(rstd, g.w * sc[k].w - mean_h - xh.w * mean_hx, res.w);
-        __stcs(out + i, o);
+        const uint2 g2 = yr[i];
+        const ulonglong2 res = rr[i];
+        uint64_t o[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint64_t g = f2_of_bf16(j == 0 ? g2.x : g2.y), xh = f2_mul(v[k][j], rs);
+          a_shift[k][j] = f2_add(a_shift[k][j], g);
+          a_scale[k][j] = f2_fma(g, xh, a_scale[k][j]);
+          o[j] = f2_fma(f2_fma(xh, nmx, f2_fma(g, sc[k][j], nmh)), rs, j == 0 ? res.x : res.y);
+        }
+        float4 w;
+        f2_unpack(o[0], w.x, w.y);
+        f2_unpack(o[1], w.z, w.w);
+        __stcs(out + i, w);
       }
     }
   }
-  float4* p0 = reinterpret_cast<float4*>(part + (long)blockIdx.x * 2 * D);
+  ulonglong2* p0 = reinterpret_cast<ulonglong2*>(part + (long)blockIdx.x * 2 * D);
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
     const int i = threadIdx.x + k * T;
     if (i < nv) {
-      p0[i] = a_shift[k];
-      p0[nv + i] = a_scale[k];
+      p0[i] = make_ulonglong2(a_shift[k][0], a_shift[k][1]);
+      p0[nv + i] = make_ulonglong2(a_scale[k][0], a_scale[k][1]);
     }
   }
 }
@@ -348,7 +366,7 @@ cudaError_t launch_adaln_bwd(const float* x, const float* mod, int branch, const
     rg.count[m] = rcount[m];
   }
   const int pad = L_pad - L < plan.ctas ? L_pad - L : plan.ctas;
-  const int grid = ch.first[3] + pad, vpt = (D / 4 + plan.threads - 1) / plan.threads;
+  const int grid = ch.first[3] + pad;
   const int bytes = plan.stages * 10 * D;
   static unsigned long long attr_done[4] = {0, 0, 0, 0};
   cudaError_t e = cudaSuccess;
@@ -360,7 +378,7 @@ cudaError_t launch_adaln_bwd(const float* x, const float* mod, int branch, const
                        ch, L, L_pad, D, eps, plan.stages, part);                                                     \
     break;                                                                                                           \
   }
-  switch (vpt) {
+  switch (plan.vpt) {
     H3_ADALN_BWD(1)
     H3_ADALN_BWD(2)
     H3_ADALN_BWD(3)

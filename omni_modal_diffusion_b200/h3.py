@@ -490,21 +490,19 @@ def _call_backward(name, dims, ranges, stream, spec, tensors, counts, at=None, v
         if t is None and optional:
             args.append(None)
             continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        if not isinstance(t, torch.Tensor) or (d := t.get_device()) < 0:
             raise TypeError(f"{n} must be a CUDA tensor")
         if t.dtype != dt:
             raise TypeError(f"{n} must be {dt}, got {t.dtype}")
         if not t.is_contiguous():
             raise ValueError(f"{n} must be contiguous")
-        if n == "ws":
-            if t.numel() < count:
-                raise ValueError(f"workspace too small: {count} bytes needed")
-        elif t.numel() != count:
-            raise ValueError(f"{n} must have {count} elements, got {t.numel()}")
-        if dev < 0:
-            dev = t.get_device()
-        elif t.get_device() != dev:
-            raise ValueError(f"{n} is on device {t.get_device()}, the others on {dev}")
+        if t.numel() != count and (n != "ws" or t.numel() < count):
+            raise ValueError(f"workspace too small: {count} bytes needed" if n == "ws" else
+                             f"{n} must have {count} elements, got {t.numel()}")
+        if d != dev:
+            if dev >= 0:
+                raise ValueError(f"{n} is on device {d}, the others on {dev}")
+            dev = d
         args.append(t.data_ptr())
     if stream is None:
         stream = torch.cuda.current_stream(dev)
