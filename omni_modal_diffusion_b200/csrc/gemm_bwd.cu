@@ -92,16 +92,18 @@ struct Cfg {
   static constexpr int ACCS = KIND == FFN ? 1 : 2;  // TMEM accumulators: 256 + 128 columns, or 2 x 256
   // Warp 0 TMA, warp 1 MMA, then EW epilogue warps: EW / 4 of each TMEM lane
   // quarter, sharing the tile's columns.  Sixteen hide the latency of the
-  // TMEM and global accesses of one tile; QKNORM needs a head's 128 columns in
-  // one warp and has eight.
-  static constexpr int EW = KIND == QKNORM ? 8 : 16;
+  // TMEM and global accesses of one tile.
+  static constexpr int EW = 16;
   // PRODUCTS: one more warp loads the tile of W that a gate's gradient needs.
   // (Five stages beside its 64 KB: 2-4% faster than four for the gated
   // product, and as fast as six for the others.)
   static constexpr int THREADS = (2 + EW + (KIND == PRODUCTS ? 1 : 0)) * 32;
   static constexpr int WTILE = KIND == PRODUCTS ? 4 * OPERAND : 0;  // 128 rows x 256 columns
   static constexpr int MISC = 768;
-  static constexpr int NORM = KIND == QKNORM ? 8 * 2 * 128 * 4 : 0;  // [epilogue warp][q, k][128]
+  // QKNORM: [epilogue warp][q, k][64] sums, and two floats of each row and warp
+  // for the exchange between the two warps of a head row, for two tiles in turn
+  // (a warp that writes one has passed the other's barrier, so both have read it)
+  static constexpr int NORM = KIND == QKNORM ? EW * 2 * 64 * 4 + 2 * EW * 32 * 8 : 0;
   static constexpr int BYTES = STAGES * STAGE + WTILE + 1024 + MISC + NORM;
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
@@ -178,21 +180,21 @@ __device__ __forceinline__ void unpack8(const uint4& u, float* f) {
   }
 }
 
-// One 32-column chunk of d(rotated q or k) of a token and head, turned back by
-// the token's angles: (a, b) = (d0 cos + d1 sin, d1 cos - d0 sin), the
+// 16 columns (from column 16 c) of d(rotated q or k) of a token and head, turned
+// back by the token's angles: (a, b) = (d0 cos + d1 sin, d1 cos - d0 sin), the
 // transpose of the forward rotation.
-__device__ __forceinline__ void unrotate32(const bf16* d, bool valid, const float* p3, const float* freq,
+__device__ __forceinline__ void unrotate16(const bf16* d, bool valid, const float* p3, const float* freq,
                                            const uint8_t* axis, int c, float* t) {
-  if (!valid) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) t[i] = 0.f;
-    return;
+  uint4 u = make_uint4(0, 0, 0, 0), v = u;
+  if (valid) {
+    u = __ldg(reinterpret_cast<const uint4*>(d + c * 16));
+    v = __ldg(reinterpret_cast<const uint4*>(d + c * 16 + 8));
   }
+  unpack8(u, t);
+  unpack8(v, t + 8);
 #pragma unroll
-  for (int j = 0; j < 32; j += 8) unpack8(__ldg(reinterpret_cast<const uint4*>(d + c * 32 + j)), t + j);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int ip = c * 16 + i, ax = axis[ip];
+  for (int i = 0; i < 8; ++i) {
+    const int ip = c * 8 + i, ax = axis[ip];
     const float pa = ax == 0 ? p3[0] : (ax == 1 ? p3[1] : p3[2]);
     float sn, cs;
     gemm_detail::rope_sincos(pa * freq[ip], &sn, &cs);
@@ -201,20 +203,30 @@ __device__ __forceinline__ void unrotate32(const bf16* d, bool valid, const floa
     t[2 * i + 1] = b * cs - a * sn;
   }
 }
+__device__ __forceinline__ void unpack16(const bf16* w, float* f) {
+  unpack8(__ldg(reinterpret_cast<const uint4*>(w)), f);
+  unpack8(__ldg(reinterpret_cast<const uint4*>(w + 8)), f + 8);
+}
 
 // RMSNorm backward of one head row: x raw (TMEM), xhat = x inv, dh = t (.) w,
 // dx = inv (dh - xhat mean(dh xhat)); with s = sum dh x, mean(dh xhat) =
-// s inv / 128.  Two passes over the row's four chunks; sum_t t xhat, the
-// gradient of w, goes to wacc[128] of this warp.
+// s inv / 128.  Two warps take 64 columns of the row each, in two passes, and
+// exchange their sums of x^2 and dh x between them (xch, one float2 a row and
+// warp, of this tile; `bar` of the two at phase `parity`).  sum_t t xhat, the
+// gradient of w, goes to wacc[2][64] of this warp.  False: a wait gave up.
+// (Chunks of 16 columns in loops that are not unrolled: unrolled, the code was
+// some 80 KB and the first tile of a small call spent most of its time
+// fetching it.)
 template <typename Release>
-__device__ __forceinline__ void epi_qknorm(const Params& p, uint32_t tb, int m, int n, int I, const float* freq,
-                                           const uint8_t* axis, float* wacc2, Release release) {
+__device__ __forceinline__ bool epi_qknorm(const Params& p, uint32_t tb, int m, int n, int I, const float* freq,
+                                           const uint8_t* axis, float* wacc2, float2* xch, int half, uint64_t* bar,
+                                           uint32_t parity, Release release) {
   const int lane = threadIdx.x & 31;
-  const int part = n / I, hd = (n % I) / 128;
+  const int part = n / I, hd = (n % I) / 128, c0 = half * 4;  // 16-column chunks [c0, c0 + 4) of the head
   const bool valid = m < p.rows;
   const bf16* d = (part == 0 ? p.dq : p.dk) + ((long)hd * p.L_pad + (valid ? m : 0)) * 128;
   const bf16* w = part == 0 ? p.qn_w : p.kn_w;
-  float* wacc = wacc2 + part * 128;
+  float* wacc = wacc2 + part * 64;
   float p3[3] = {0.f, 0.f, 0.f};
   if (valid) {
     p3[0] = p.pos[(long)m * 3];
@@ -224,58 +236,57 @@ __device__ __forceinline__ void epi_qknorm(const Params& p, uint32_t tb, int m, 
   float ss = 0.f, s = 0.f;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
-    float x[32], t[32];
-    ld_chunk(tb + c * 32, x);
-    unrotate32(d, valid, p3, freq, axis, c, t);
+    float x[16], t[16], wv[16];
+    ld_chunk16(tb + c * 16, x);
+    unrotate16(d, valid, p3, freq, axis, c0 + c, t);
+    unpack16(w + (c0 + c) * 16, wv);
     tmem_wait_ld();
 #pragma unroll
-    for (int j = 0; j < 32; j += 8) {
-      float wv[8];
-      unpack8(__ldg(reinterpret_cast<const uint4*>(w + c * 32 + j)), wv);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        ss = fmaf(x[j + i], x[j + i], ss);
-        s = fmaf(t[j + i] * wv[i], x[j + i], s);
-      }
+    for (int j = 0; j < 16; ++j) {
+      ss = fmaf(x[j], x[j], ss);
+      s = fmaf(t[j] * wv[j], x[j], s);
     }
   }
-  const float inv = rsqrtf(ss * (1.0f / 128.0f) + p.eps_qk);
-  const float mean = s * inv * (1.0f / 128.0f);
-  uint32_t out[64];
-#pragma unroll
+  // the two halves' sums, added in the same order by both warps
+  xch[half * 32 + lane] = make_float2(ss, s);
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+  if (!mbar_wait_warp(bar, parity)) return false;
+  const float2 lo = xch[lane], hi = xch[32 + lane];
+  const float inv = rsqrtf((lo.x + hi.x) * (1.0f / 128.0f) + p.eps_qk);
+  const float mean = (lo.y + hi.y) * inv * (1.0f / 128.0f);
+  bf16* dst = p.dqkv + (long)m * 3 * p.I + n + half * 64;
+#pragma unroll 1
   for (int c = 0; c < 4; ++c) {
-    float x[32], t[32];
-    ld_chunk(tb + c * 32, x);
-    unrotate32(d, valid, p3, freq, axis, c, t);
+    float x[16], t[16], wv[16];
+    ld_chunk16(tb + c * 16, x);
+    unrotate16(d, valid, p3, freq, axis, c0 + c, t);
+    unpack16(w + (c0 + c) * 16, wv);
     tmem_wait_ld();
+    if (c == 3) release();
 #pragma unroll
-    for (int j = 0; j < 32; j += 8) {
-      float wv[8];
-      unpack8(__ldg(reinterpret_cast<const uint4*>(w + c * 32 + j)), wv);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float xh = x[j + i] * inv;
-        x[j + i] = inv * (t[j + i] * wv[i] - xh * mean);
-        t[j + i] *= xh;
-      }
+    for (int j = 0; j < 16; ++j) {
+      const float xh = x[j] * inv;
+      x[j] = inv * (t[j] * wv[j] - xh * mean);
+      t[j] *= xh;
     }
-    pack_row<32>(x, out + c * 16);
-    // sum over the warp's 32 rows: lane l ends with column l of the chunk
+    uint32_t out[8];
+    pack_row<16>(x, out);
+    store16(dst + c * 16, 3L * p.I, m, p.rows, out);
+    // sum over the warp's 32 rows: lanes 2l and 2l + 1 end with column l
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int o = 16; o > 1; o >>= 1) {
       const bool up = (lane & o) != 0;
 #pragma unroll
-      for (int i = 0; i < o; ++i) {
-        const float send = up ? t[i] : t[i + o], keep = up ? t[i + o] : t[i];
+      for (int i = 0; i < o / 2; ++i) {
+        const float send = up ? t[i] : t[i + o / 2], keep = up ? t[i + o / 2] : t[i];
         t[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
       }
     }
-    wacc[c * 32 + lane] += t[0];
+    t[0] += __shfl_xor_sync(0xffffffffu, t[0], 1);
+    if ((lane & 1) == 0) wacc[c * 16 + (lane >> 1)] += t[0];
   }
-  release();
-  bf16* dst = p.dqkv + (long)m * 3 * p.I + n;
-#pragma unroll
-  for (int c = 0; c < 8; ++c) store16(dst + c * 16, 3L * p.I, m, p.rows, out + c * 8);
+  return true;
 }
 
 // h = SiLU(g) u, du = dh SiLU(g), dg = dh u sig(g) (1 + g (1 - sig(g))) for 32 of
@@ -366,6 +377,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 3);
   float* freq = reinterpret_cast<float*>(tmem_slot + 4);
   uint8_t* axis = reinterpret_cast<uint8_t*>(freq + 64);
+  uint64_t* xbar = reinterpret_cast<uint64_t*>(axis + 64);  // QKNORM: [8] two warps of a head row
   float* wacc = reinterpret_cast<float*>(smem + STAGES * STAGE + C::WTILE + C::MISC);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -385,6 +397,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
     mbar_init(drain, 1);
     mbar_init(w_full, 1);
     mbar_init(w_empty, EW);
+    for (int i = 0; i < 8; ++i) mbar_init(&xbar[i], 2);
     fence_mbar_init();
     for (int i = 0; i < p.n_maps; ++i) tma_prefetch_desc(&maps.m[i]);
   }
@@ -403,7 +416,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       freq[i] = powf(p.theta, -2.0f * (float)i_sec / (float)d_sec);
       axis[i] = (uint8_t)ax;
     }
-    for (int i = threadIdx.x; i < 8 * 2 * 128; i += C::THREADS) wacc[i] = 0.f;
+    for (int i = threadIdx.x; i < EW * 128; i += C::THREADS) wacc[i] = 0.f;
   }
   tc_fence_before();
   __syncthreads();
@@ -444,20 +457,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
               uint8_t* sA = smem + stage * STAGE;
               uint8_t* sB = sA + OPERAND;
               if constexpr (A_MN) {
-                tma_load_2d_pair(sA, ma, fb, a0, kb * BK);
-                tma_load_2d_pair(sA + OPERAND / 2, ma, fb, a0 + 64, kb * BK);
+                tma_load_3d_pair(sA, ma, fb, 0, kb * BK, a0 / 64);
               } else {
                 tma_load_2d_pair(sA, ma, fb, kb * BK, a0);
               }
               if constexpr (KIND == PRODUCTS) {
-                tma_load_2d_pair(sB, mb, fb, b0, kb * BK);
-                tma_load_2d_pair(sB + OPERAND / 2, mb, fb, b0 + 64, kb * BK);
+                tma_load_3d_pair(sB, mb, fb, 0, kb * BK, b0 / 64);
               } else {
                 tma_load_2d_pair(sB, mb, fb, kb * BK, b0);
               }
               if constexpr (KIND == FFN) {
                 tma_load_2d_pair(sA + 2 * OPERAND, &maps.m[2], fb, kb * BK, a0);
-                tma_load_2d_pair(sA + 3 * OPERAND, &maps.m[3], fb, d0, kb * BK);
+                tma_load_3d_pair(sA + 3 * OPERAND, &maps.m[3], fb, 0, kb * BK, d0 / 64);
               }
               ++issued;
               if (++stage == STAGES) { stage = 0; phase ^= 1; }
@@ -544,9 +555,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         if (!pr.gated) continue;
         if (!mbar_wait(w_empty, (n & 1) ^ 1)) break;
         mbar_arrive_expect_tx(w_full, C::WTILE);
-        for (int c = 0; c < 4; ++c)
-          tma_load_2d(sW + c * OPERAND, &maps.m[pr.map0 + 6], w_full, w.nt * 256 + c * 64,
-                      w.mt * 256 + (int)rank * 128);
+        tma_load_3d(sW, &maps.m[pr.map0 + 6], w_full, 0, w.mt * 256 + (int)rank * 128, w.nt * 4);
         ++n;
       }
       if (n > 0) mbar_wait(w_full, (n - 1) & 1);
@@ -582,8 +591,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         epi_ffn(p, tmem_base + lane_off + (uint32_t)(acc * 256), m, w.nt, sub, release);
       } else if constexpr (KIND == QKNORM) {
         if (!wait_full()) break;
-        epi_qknorm(p, tmem_base + lane_off + (uint32_t)(acc * 256 + sub * COLS), m, n0, pr.N / 2, freq, axis,
-                   wacc + (warp - 2) * 256, release);
+        // sub 0, 1 and 2, 3 share the tile's two heads
+        const int two = (sub >> 1) * 4 + q;
+        float2* xch = reinterpret_cast<float2*>(wacc + EW * 128) + (n_w & 1) * EW * 32 + two * 64;
+        ok = epi_qknorm(p, tmem_base + lane_off + (uint32_t)(acc * 256 + sub * COLS), m, w.nt * 256 + (sub >> 1) * 128,
+                        pr.N / 2, freq, axis, wacc + (warp - 2) * 128, xch, sub & 1, &xbar[two], n_w & 1, release);
+        if (!ok) break;
+        ++n_w;
       } else if (pr.gated) {
         // the warp's 64 output columns of this row stay in registers while the
         // modalities' accumulators come by; W's 64 columns (one swizzled box)
@@ -661,10 +675,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
   tc_fence_before();
   __syncthreads();
   if constexpr (KIND == QKNORM) {
-    if (threadIdx.x < 256) {
+    if (threadIdx.x < 256) {  // column c of q or k: the warps whose half of the head holds it
+      const int part = threadIdx.x >> 7, c = threadIdx.x & 127;
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) s += wacc[w * 256 + threadIdx.x];
+      for (int w = 0; w < EW; ++w)
+        if (((w >> 2) & 1) == c >> 6) s += wacc[w * 128 + part * 64 + (c & 63)];
       p.w_part[(long)blockIdx.x * 256 + threadIdx.x] = s;
     }
   }
@@ -706,12 +722,24 @@ size_t split_bytes(int M, int N, int num_kb) {
   return s > 1 ? ((size_t)s * M * N * 4 + 255) / 256 * 256 : 0;
 }
 
-// K-major operand: rows x cols, 128-row boxes; MN-major: 64-row boxes
+// K-major operand: rows x cols in 128-row boxes
 bool map_k(CUtensorMap* m, const void* base, long rows, long cols, long ld) {
   return make_tmap_bf16(m, base, rows, cols, ld, 128);
 }
-bool map_mn(CUtensorMap* m, const void* base, long rows, long cols, long ld) {
-  return make_tmap_bf16(m, base, rows, cols, ld, 64);
+// MN-major operand: its columns (a multiple of 64) as blocks of 64, the
+// outermost dimension, so that one load of `blocks` of them fills an operand,
+// each block's rows together as the swizzled layout wants them (3% fewer SM
+// cycles over the backward calls than a load for each block).
+bool map_mn(CUtensorMap* m, const void* base, long rows, long cols, int box_rows, int blocks) {
+  gemm_detail::EncodeTiledFn fn = gemm_detail::encode_fn();
+  if (!fn) return false;
+  cuuint64_t gdim[3] = {64, (cuuint64_t)rows, (cuuint64_t)cols / 64};
+  cuuint64_t gstride[2] = {(cuuint64_t)cols * 2, 128};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)blocks};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), gdim, gstride, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 void set_tiles(Product& pr, int M, int N, int n_step) {
@@ -784,7 +812,7 @@ struct Products {
     using namespace gemm_bwd;
     Product& pr = add(out_rows, N, 1, plan_splits(out_rows, N, K / gemm_bwd::BK), out);
     pr.kb[0] = K / gemm_bwd::BK;
-    good = good && map_k(&maps.m[n_maps], A, rows, K, K) && map_mn(&maps.m[n_maps + 1], B, K, N, N);
+    good = good && map_k(&maps.m[n_maps], A, rows, K, K) && map_mn(&maps.m[n_maps + 1], B, K, N, gemm_bwd::BK, 2);
     n_maps += 2;
   }
   // out [M][N] = A [rows][M]^T B [rows][N]
@@ -793,7 +821,8 @@ struct Products {
     Product& pr = add(M, N, 1, plan_splits(M, N, L_pad / gemm_bwd::BK), out);
     pr.a_mn = 1;
     pr.kb[0] = (rows + gemm_bwd::BK - 1) / gemm_bwd::BK;
-    good = good && map_mn(&maps.m[n_maps], A, rows, M, M) && map_mn(&maps.m[n_maps + 1], B, rows, N, N);
+    good = good && map_mn(&maps.m[n_maps], A, rows, M, gemm_bwd::BK, 2) &&
+           map_mn(&maps.m[n_maps + 1], B, rows, N, gemm_bwd::BK, 2);
     n_maps += 2;
   }
   // dW [M][N] = sum_m gate_m (.) A_m^T B_m over the modality ranges (null: not
@@ -807,10 +836,10 @@ struct Products {
     for (int m = 0; m < 3; ++m) {
       pr.kb[m] = (count[m] + gemm_bwd::BK - 1) / gemm_bwd::BK;
       if (count[m] == 0) continue;
-      good = good && map_mn(&maps.m[n_maps + m], A + (long)start[m] * M, count[m], M, M) &&
-             map_mn(&maps.m[n_maps + 3 + m], B + (long)start[m] * N, count[m], N, N);
+      good = good && map_mn(&maps.m[n_maps + m], A + (long)start[m] * M, count[m], M, gemm_bwd::BK, 2) &&
+             map_mn(&maps.m[n_maps + 3 + m], B + (long)start[m] * N, count[m], N, gemm_bwd::BK, 2);
     }
-    good = good && map_k(&maps.m[n_maps + 6], W, M, N, N);
+    good = good && map_mn(&maps.m[n_maps + 6], W, M, N, 128, 4);
     n_maps += 7;
     p.mod = mod;
     p.gate_slot = slot;
@@ -846,7 +875,7 @@ cudaError_t launch_ffn_bwd(const bf16* xm, const bf16* dy, const bf16* Wgu, cons
   memset(&maps, 0, sizeof(maps));
   memset(&p, 0, sizeof(p));
   if (!map_k(&maps.m[0], xm, rows, D, D) || !map_k(&maps.m[1], Wgu, 2 * F, D, D) ||
-      !map_k(&maps.m[2], dy, rows, D, D) || !map_mn(&maps.m[3], Wd, D, F, F))
+      !map_k(&maps.m[2], dy, rows, D, D) || !map_mn(&maps.m[3], Wd, D, F, gemm_bwd::BK, 1))
     return cudaErrorInvalidValue;
   p.n_products = 1;
   Product& pr = p.pr[0];
