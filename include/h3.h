@@ -545,7 +545,8 @@ int h3_attention_sp(const h3_dims* dims, const h3_sp_layout* layout, const h3_sp
  *     of h3_adaln_norm_modulate_backward may be dres.
  *   - Sums run in a fixed order: the same call gives the same bits.
  *   - ws: caller-owned scratch of h3_backward_workspace_bytes() bytes for the
- *     operation, 16-byte aligned; nothing in it outlives the call's kernels. */
+ *     operation, 16-byte aligned; nothing in it outlives the call's kernels.
+ *     Calls that may run at the same time (other streams) need one each. */
 enum h3_backward_op {
   H3_BWD_ADALN = 0,
   H3_BWD_QKV = 1,

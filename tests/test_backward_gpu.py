@@ -326,6 +326,100 @@ def test_ffn_saturated_gates():
         inside(got, w, name)
 
 
+# ---------------------------------------------------------------- long sequences
+
+LONG = (512, 1200, 122304)  # the packed 15 s sequence: 124,016 tokens
+
+
+def test_attention_long():
+    """One head over 124,016 tokens: dq of sampled queries and dk, dv of sampled
+    keys (the last ones of the ragged tile among them) against float64 on the
+    GPU, lse of every row."""
+    t = Inputs(LONG, 64, 1, 128, seed=111, fill=0.0)
+    L = t.L
+    g = torch.Generator(device=DEV)
+    g.manual_seed(111)
+    draw = lambda std: torch.empty(1, t.Lp, 128, device=DEV).normal_(0, std, generator=g)  # noqa: E731
+    unit = lambda x: x * torch.rsqrt(x.square().mean(-1, keepdim=True))  # noqa: E731
+    q, k, v, do = (x.to(BF16) for x in (unit(draw(1.0)), unit(draw(1.0)), draw(1.0), draw(1e-2)))
+    for x in (q, k, v, do):
+        x[:, L:] = 0
+    one = torch.ones(128, dtype=BF16, device=DEV)
+    o, lse, do = t.empty(t.Lp, 128), t.empty(1, t.Lp, dtype=F32), do.view(t.Lp, 128)
+    h3.h3_attention_lse(t.dims, t.ranges, q, k, v, o, lse, qn_w=one, kn_w=one)
+    dq, dk, dv = (t.empty(1, t.Lp, 128) for _ in range(3))
+    h3.h3_attention_backward(t.dims, t.ranges, q, k, v, o, lse, do, dq, dk, dv, t.ws(h3.H3_BWD_ATTENTION))
+    t.finish()
+    Q, K, V, DO = (x.view(t.Lp, 128)[:L].double() for x in (q, k, v, do))
+    c = 128 ** -0.5
+    ref_lse, O_ = [], []
+    for i in range(0, L, 4096):
+        s = c * (Q[i:i + 4096] @ K.T)
+        ref_lse.append(torch.logsumexp(s, 1))
+        O_.append(torch.exp(s - ref_lse[-1][:, None]) @ V)
+    ref_lse, O_ = torch.cat(ref_lse), torch.cat(O_)
+    # fp32 sums of 124,016 exponentials of scores below 12
+    assert (lse[0, :L].double() - ref_lse).abs().max() <= 2.0 ** -16
+    delta = (DO * O_).sum(1)
+    rows = torch.cat((torch.arange(0, L, L // 61, device=DEV), torch.arange(L - 5, L, device=DEV)))
+    p = torch.exp(c * (Q[rows] @ K.T) - ref_lse[rows, None])
+    want = c * ((p * (DO[rows] @ V.T - delta[rows, None])) @ K)
+    pk = torch.exp(c * (Q @ K[rows].T) - ref_lse[:, None])
+    want_dv = pk.T @ DO
+    want_dk = c * ((pk * (DO @ V[rows].T - delta[:, None])).T @ Q)
+    for name, got, ref in (("dq", dq, want), ("dk", dk, want_dk), ("dv", dv, want_dv)):
+        off = (got[0, rows].double() - ref).norm() / ref.norm()
+        assert off <= 3 * U, (name, float(off))  # P, dS and o, and the result: three roundings each
+        assert torch.all(got[0, L:] == 0)
+
+
+def test_products_long():
+    """124,016 tokens through narrow layers: contractions over the tokens in
+    splits."""
+    t = Inputs(LONG, 64, 1, 128, seed=121)
+    dx, xm, mod = t.normal(t.L, 64, bf16=False), t.normal(t.L, 64), mod_with_zero_gates(t)
+    Wgu, Wd = t.normal(256, 64, std=0.2), t.normal(64, 128, std=0.1)
+    dxm, dWgu, dWd, dmod = t.empty(t.Lp, 64), t.empty(256, 64), t.empty(64, 128), t.empty(3, 6, 64)
+    h3.h3_ffn_swiglu_backward(t.dims, t.ranges, t.rows(dx, F32), t.rows(xm), dev(Wgu), dev(Wd), dev(mod, F32), dxm,
+                              dWgu, dWd, dmod, t.ws(h3.H3_BWD_FFN))
+    t.finish()
+    want = G.ffn_swiglu(dx, xm, Wgu, Wd, mod, t.r, err=True)
+    for got, w, name in zip((dxm[:t.L], dWgu, dWd, dmod[:, 5]), want, ("dxm", "dWgu", "dWd", "dgate")):
+        inside(got, w, name, 3)
+    check_adaln(t, 0, t.normal(t.L, 64, std=3.0, bf16=False), t.normal(3, 6, 64, std=0.1, bf16=False),
+                t.normal(t.L, 64), t.normal(t.L, 64, bf16=False))
+
+
+def test_gated_residual_wide_and_long():
+    """124,016 tokens at full width, where byte offsets pass 2^31: sampled rows
+    of do, and of dWo and the gate sampled channels, against float64 on the GPU."""
+    t = Inputs(LONG, 5376, 56, 128, seed=131, fill=0.0)
+    L, D, I = t.L, t.D, t.I
+    g = torch.Generator(device=DEV)
+    g.manual_seed(131)
+    normal = lambda *s, std=1.0, dt=BF16: torch.empty(*s, device=DEV, dtype=dt).normal_(0, std, generator=g)  # noqa: E731
+    dx, o, Wo, mod = normal(t.Lp, D, dt=F32), normal(t.Lp, I), normal(D, I, std=0.02), normal(3, 6, D, dt=F32)
+    do, dWo, dmod = t.empty(t.Lp, I), t.empty(D, I), t.empty(3, 6, D)
+    h3.h3_gated_residual_backward(t.dims, t.ranges, dx, o, Wo, mod, do, dWo, dmod, t.ws(h3.H3_BWD_GATED_RESIDUAL))
+    t.finish()
+    gate = torch.repeat_interleave(mod[:, 2], torch.tensor(LONG, device=DEV), dim=0)
+    rows = torch.cat((torch.arange(0, L, 4001, device=DEV), torch.arange(L - 3, L, device=DEV)))
+    ref = (dx[rows] * gate[rows]).double() @ Wo.double()
+    assert (do[rows].double() - ref).norm() <= 2 * U * ref.norm()
+    assert torch.all(do[L:] == 0)
+    ch = torch.tensor([0, 1, 127, 128, 2500, D - 1], device=DEV)
+    dW = torch.zeros(len(ch), I, device=DEV, dtype=torch.float64)
+    G_ = torch.zeros(3, len(ch), I, device=DEV, dtype=torch.float64)
+    for m, (a, n) in enumerate(zip((0, 512, 1712), LONG)):
+        for i in range(a, a + n, 8192):
+            e = min(i + 8192, a + n)
+            G_[m] += dx[i:e, ch].double().T @ o[i:e].double()
+        dW += mod[m, 2, ch].double()[:, None] * G_[m]
+    assert (dWo[ch].double() - dW).norm() <= 2 * U * dW.norm()
+    dg = (G_ * Wo[ch].double()).sum(2)
+    assert (dmod[:, 2, ch].double() - dg).norm() <= 2 * U * dg.norm()
+
+
 # ---------------------------------------------------------------- frozen weights
 
 def test_gradients_that_are_not_wanted_are_not_written():
