@@ -36,6 +36,18 @@ struct AdalnPlan {
 static AdalnPlan adaln_plan(int D) {
   AdalnPlan p;
   const int nv = D / 4;
+  if (nv <= 128) {
+    // narrow rows: one warp a row, no barrier in its reductions, and as many
+    // of them as fit with four stages and 1.5 KB each (26,857 rows of 256:
+    // 49 us with a CTA of 64 threads a row, 29 us so)
+    p.vpt = (nv + 31) / 32;
+    p.threads = 32;
+    p.stages = AB_STAGES;
+    const int fit = 225 * 1024 / (AB_STAGES * 10 * D + 1536);
+    p.per_sm = fit < 16 ? fit : 16;
+    p.ctas = 148 * p.per_sm;
+    return p;
+  }
   p.vpt = (nv + AB_MAX_THREADS - 1) / AB_MAX_THREADS;
   p.threads = ((nv + p.vpt - 1) / p.vpt + 31) / 32 * 32;
   p.per_sm = 1024 / p.threads;
@@ -61,6 +73,10 @@ __device__ __forceinline__ void block_sums(float* v, float* red) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   const int w = threadIdx.x / 32, l = threadIdx.x % 32, nw = blockDim.x / 32;
+  if (nw == 1) {
+    __syncwarp();
+    return;
+  }
   if (l == 0) {
 #pragma unroll
     for (int i = 0; i < N; ++i) red[i * 16 + w] = v[i];
@@ -217,42 +233,46 @@ __global__ void __launch_bounds__(AB_MAX_THREADS, VPT <= 3 ? 2 : 1) adaln_bwd_ke
 
 // ------------------------------------------------------------ partial sums
 // out[m][c] = bf16(sum of part[p * stride + m * offset + c] over p in [begin[m],
-// end[m])), c < cols, for the blockIdx.y-th m.  A CTA takes 32 columns; its
-// eight warps take every eighth partial and their sums are added in order.
+// end[m])), c < cols, for the blockIdx.y-th m.  A CTA takes 32 columns; its W
+// warps take every W-th partial, eight at a time, and their sums are added in
+// order.
 struct Parts {
   int begin[3], end[3];
   bf16* out[3];  // null: not wanted
 };
+template <int W>
 __device__ __forceinline__ void reduce_parts(const float* __restrict__ part, const Parts& pp, int m, long stride,
                                              long offset, int cols, int block, float (*acc)[32]) {
   const int c = block * 32 + (threadIdx.x & 31), w = threadIdx.x / 32;
-  part += m * offset;
+  part += m * offset + c;
   float s = 0.f;
   if (c < cols && pp.out[m] != nullptr) {
     int p = pp.begin[m] + w;
     const int end = pp.end[m];
-    for (; p + 24 < end; p += 32) {
-      const float a = part[p * stride + c], b = part[(p + 8) * stride + c], d = part[(p + 16) * stride + c],
-                  e = part[(p + 24) * stride + c];
-      s += (a + b) + (d + e);
+    for (; p + 7 * W < end; p += 8 * W) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = part[(p + k * W) * stride];
+      s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
     }
-    for (; p < end; p += 8) s += part[p * stride + c];
+    for (; p < end; p += W) s += part[p * stride];
   }
   acc[w][threadIdx.x & 31] = s;
   __syncthreads();
   if (w == 0 && c < cols && pp.out[m] != nullptr) {
     float t = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) t += acc[k][threadIdx.x];
+    for (int k = 0; k < W; ++k) t += acc[k][threadIdx.x];
     pp.out[m][c] = __float2bfloat16_rn(t);
   }
 }
-__global__ void __launch_bounds__(256) reduce_parts_kernel(const float* __restrict__ part,
-                                                           const __grid_constant__ Parts pp, long stride, long offset,
-                                                           int cols) {
-  __shared__ float acc[8][32];
+template <int W>
+__global__ void __launch_bounds__(W * 32) reduce_parts_kernel(const float* __restrict__ part,
+                                                              const __grid_constant__ Parts pp, long stride,
+                                                              long offset, int cols) {
+  __shared__ float acc[W][32];
   chain_wait();
-  reduce_parts(part, pp, blockIdx.y, stride, offset, cols, blockIdx.x, acc);
+  reduce_parts<W>(part, pp, blockIdx.y, stride, offset, cols, blockIdx.x, acc);
 }
 
 // What is left after the products of a backward call: the sums of the split
@@ -279,7 +299,7 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Fin
   const int b = blockIdx.x;
   if (b >= f.first[f.n_sums]) {
     const int r = b - f.first[f.n_sums];
-    reduce_parts(f.reduce_part, f.reduce, r / f.reduce_ctas, f.reduce_stride, f.reduce_offset, f.reduce_cols,
+    reduce_parts<8>(f.reduce_part, f.reduce, r / f.reduce_ctas, f.reduce_stride, f.reduce_offset, f.reduce_cols,
                  r % f.reduce_ctas, acc);
     return;
   }
@@ -356,6 +376,7 @@ cudaError_t launch_adaln_bwd(const float* x, const float* mod, int branch, const
   // as few rows per CTA as let the three modalities' CTAs, whose last ones may
   // be short, run in one wave
   ch.rows = (L + plan.ctas - 1) / plan.ctas;
+  if (plan.threads == 32 && L > 1024 && ch.rows < 4) ch.rows = 4;  // fewer partials than a warp a row would leave
   for (;; ++ch.rows) {
     ch.first[0] = 0;
     for (int m = 0; m < 3; ++m) ch.first[m + 1] = ch.first[m] + (rcount[m] + ch.rows - 1) / ch.rows;
@@ -395,7 +416,12 @@ cudaError_t launch_adaln_bwd(const float* x, const float* mod, int branch, const
     pp.end[m] = ch.first[m + 1];
     pp.out[m] = dmod + (long)(m * 6 + 3 * branch) * D;
   }
-  return launch_chained(reduce_parts_kernel, dim3((2 * D + 31) / 32, 3), 256, 0, stream, part, pp, 2L * D, 0L, 2 * D);
+  const dim3 grid_r((2 * D + 31) / 32, 3);
+  // eight warps a CTA, or 32 where they would walk more than 32 partials each
+  // (2,368 partials of 512 columns: 12 us with eight, 5 us with 32)
+  if (ch.first[3] > 256)
+    return launch_chained(reduce_parts_kernel<32>, grid_r, 1024, 0, stream, part, pp, 2L * D, 0L, 2 * D);
+  return launch_chained(reduce_parts_kernel<8>, grid_r, 256, 0, stream, part, pp, 2L * D, 0L, 2 * D);
 }
 
 // One launch for all of it (none if nothing is left)

@@ -100,10 +100,10 @@ struct Cfg {
   static constexpr int THREADS = (2 + EW + (KIND == PRODUCTS ? 1 : 0)) * 32;
   static constexpr int WTILE = KIND == PRODUCTS ? 4 * OPERAND : 0;  // 128 rows x 256 columns
   static constexpr int MISC = 768;
-  // QKNORM: [epilogue warp][q, k][64] sums, and two floats of each row and warp
-  // for the exchange between the two warps of a head row, for two tiles in turn
-  // (a warp that writes one has passed the other's barrier, so both have read it)
-  static constexpr int NORM = KIND == QKNORM ? EW * 2 * 64 * 4 + 2 * EW * 32 * 8 : 0;
+  // QKNORM: [epilogue warp][q, k][32] sums, and two floats of each row, head and
+  // warp for the exchange between a row's four warps, for two tiles in turn (a
+  // warp that writes one has passed the other's barrier, so all have read it)
+  static constexpr int NORM = KIND == QKNORM ? EW * 64 * 4 + 2 * EW * 2 * 32 * 8 : 0;
   static constexpr int BYTES = STAGES * STAGE + WTILE + 1024 + MISC + NORM;
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
@@ -120,8 +120,10 @@ __device__ __forceinline__ void ld_chunk16(uint32_t taddr, float* v) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
+// (L1::no_allocate: what is left of L1 beside the stages serves the loads; 9%
+// of a weight gradient over 64 tokens, which is bound by its stores)
 __device__ __forceinline__ void st_v4(uint32_t* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+  asm volatile("st.global.L1::no_allocate.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 // 8 words of row m (lane = m % 32): 16 bf16 or 8 fp32 columns; ld in words.
 // Lanes 2i and 2i + 1 exchange halves so that each store instruction writes
@@ -180,111 +182,145 @@ __device__ __forceinline__ void unpack8(const uint4& u, float* f) {
   }
 }
 
-// 16 columns (from column 16 c) of d(rotated q or k) of a token and head, turned
-// back by the token's angles: (a, b) = (d0 cos + d1 sin, d1 cos - d0 sin), the
-// transpose of the forward rotation.
-__device__ __forceinline__ void unrotate16(const bf16* d, bool valid, const float* p3, const float* freq,
-                                           const uint8_t* axis, int c, float* t) {
-  uint4 u = make_uint4(0, 0, 0, 0), v = u;
-  if (valid) {
-    u = __ldg(reinterpret_cast<const uint4*>(d + c * 16));
-    v = __ldg(reinterpret_cast<const uint4*>(d + c * 16 + 8));
-  }
-  unpack8(u, t);
-  unpack8(v, t + 8);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int ip = c * 8 + i, ax = axis[ip];
-    const float pa = ax == 0 ? p3[0] : (ax == 1 ? p3[1] : p3[2]);
-    float sn, cs;
-    gemm_detail::rope_sincos(pa * freq[ip], &sn, &cs);
-    const float a = t[2 * i], b = t[2 * i + 1];
-    t[2 * i] = a * cs + b * sn;
-    t[2 * i + 1] = b * cs - a * sn;
-  }
-}
 __device__ __forceinline__ void unpack16(const bf16* w, float* f) {
   unpack8(__ldg(reinterpret_cast<const uint4*>(w)), f);
   unpack8(__ldg(reinterpret_cast<const uint4*>(w + 8)), f + 8);
 }
 
-// RMSNorm backward of one head row: x raw (TMEM), xhat = x inv, dh = t (.) w,
-// dx = inv (dh - xhat mean(dh xhat)); with s = sum dh x, mean(dh xhat) =
-// s inv / 128.  Two warps take 64 columns of the row each, in two passes, and
-// exchange their sums of x^2 and dh x between them (xch, one float2 a row and
-// warp, of this tile; `bar` of the two at phase `parity`).  sum_t t xhat, the
-// gradient of w, goes to wacc[2][64] of this warp.  False: a wait gave up.
-// (Chunks of 16 columns in loops that are not unrolled: unrolled, the code was
-// some 80 KB and the first tile of a small call spent most of its time
-// fetching it.)
-template <typename Release>
-__device__ __forceinline__ bool epi_qknorm(const Params& p, uint32_t tb, int m, int n, int I, const float* freq,
-                                           const uint8_t* axis, float* wacc2, float2* xch, int half, uint64_t* bar,
-                                           uint32_t parity, Release release) {
+// RoPE and RMSNorm backward of the tile's two heads at one token.  With d the
+// gradient of the rotated head, t = d turned back by the token's angles
+// ((a, b) = (d0 cos + d1 sin, d1 cos - d0 sin), the transpose of the forward
+// rotation), x the head before its norm (TMEM), xhat = x inv, dh = t (.) w:
+//   dx = inv (dh - xhat mean(dh xhat));  with s = sum dh x, mean = s inv / 128
+// and the gradient of w is sum_t t xhat.
+// Four warps share a token's heads, 32 columns of both each, so that an angle's
+// sine and cosine serve both heads; two passes, with the sums of x^2 and dh x
+// exchanged between the four after the first (xch[4 warps][2 heads][32 lanes]
+// of this tile; `bar` at phase `parity`).  wacc[q, k][32] of this warp takes the
+// sums over its rows.  Loops that are not unrolled: unrolled, the code was some
+// 80 KB and the first tile of a small call spent most of its time fetching it.
+// False: a wait gave up.
+template <typename Wait, typename Release>
+__device__ __forceinline__ bool epi_qknorm(const Params& p, uint32_t tb, int m, int n0, int I, int sub,
+                                           const float* freq, const uint8_t* axis, float* wacc, float2* xch,
+                                           uint64_t* bar, uint32_t parity, Wait wait, Release release) {
   const int lane = threadIdx.x & 31;
-  const int part = n / I, hd = (n % I) / 128, c0 = half * 4;  // 16-column chunks [c0, c0 + 4) of the head
   const bool valid = m < p.rows;
-  const bf16* d = (part == 0 ? p.dq : p.dk) + ((long)hd * p.L_pad + (valid ? m : 0)) * 128;
-  const bf16* w = part == 0 ? p.qn_w : p.kn_w;
-  float* wacc = wacc2 + part * 64;
+  const bf16 *d[2], *w[2];
+  int part[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int n = n0 + h * 128, hd = (n % I) / 128;
+    part[h] = n / I;
+    d[h] = (part[h] == 0 ? p.dq : p.dk) + ((long)hd * p.L_pad + (valid ? m : 0)) * 128 + sub * 32;
+    // into L2 while the accumulator is awaited
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(d[h]));
+    w[h] = (part[h] == 0 ? p.qn_w : p.kn_w) + sub * 32;
+  }
+  tb += sub * 32;
   float p3[3] = {0.f, 0.f, 0.f};
   if (valid) {
     p3[0] = p.pos[(long)m * 3];
     p3[1] = p.pos[(long)m * 3 + 1];
     p3[2] = p.pos[(long)m * 3 + 2];
   }
-  float ss = 0.f, s = 0.f;
-#pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    float x[16], t[16], wv[16];
-    ld_chunk16(tb + c * 16, x);
-    unrotate16(d, valid, p3, freq, axis, c0 + c, t);
-    unpack16(w + (c0 + c) * 16, wv);
-    tmem_wait_ld();
+  // sine and cosine of the 8 pairs of columns [16 c, 16 c + 16) of the warp's 32
+  auto angles = [&](int c, float* cs, float* sn) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      ss = fmaf(x[j], x[j], ss);
-      s = fmaf(t[j] * wv[j], x[j], s);
+    for (int i = 0; i < 8; ++i) {
+      const int ip = sub * 16 + c * 8 + i, ax = axis[ip];
+      const float pa = ax == 0 ? p3[0] : (ax == 1 ? p3[1] : p3[2]);
+      gemm_detail::rope_sincos(pa * freq[ip], &sn[i], &cs[i]);
+    }
+  };
+  auto turn_back = [&](const bf16* src, const float* cs, const float* sn, float* t) {
+    uint4 u = make_uint4(0, 0, 0, 0), v = u;
+    if (valid) {
+      u = __ldg(reinterpret_cast<const uint4*>(src));
+      v = __ldg(reinterpret_cast<const uint4*>(src + 8));
+    }
+    unpack8(u, t);
+    unpack8(v, t + 8);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = t[2 * i], b = t[2 * i + 1];
+      t[2 * i] = a * cs[i] + b * sn[i];
+      t[2 * i + 1] = b * cs[i] - a * sn[i];
+    }
+  };
+  if (!wait()) return false;
+  float ss[2] = {0.f, 0.f}, s[2] = {0.f, 0.f};
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    float cs[8], sn[8];
+    angles(c, cs, sn);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float x[16], t[16], wv[16];
+      ld_chunk16(tb + h * 128 + c * 16, x);
+      turn_back(d[h] + c * 16, cs, sn, t);
+      unpack16(w[h] + c * 16, wv);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        ss[h] = fmaf(x[j], x[j], ss[h]);
+        s[h] = fmaf(t[j] * wv[j], x[j], s[h]);
+      }
     }
   }
-  // the two halves' sums, added in the same order by both warps
-  xch[half * 32 + lane] = make_float2(ss, s);
+  xch[(sub * 2) * 32 + lane] = make_float2(ss[0], s[0]);
+  xch[(sub * 2 + 1) * 32 + lane] = make_float2(ss[1], s[1]);
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
   if (!mbar_wait_warp(bar, parity)) return false;
-  const float2 lo = xch[lane], hi = xch[32 + lane];
-  const float inv = rsqrtf((lo.x + hi.x) * (1.0f / 128.0f) + p.eps_qk);
-  const float mean = (lo.y + hi.y) * inv * (1.0f / 128.0f);
-  bf16* dst = p.dqkv + (long)m * 3 * p.I + n + half * 64;
+  float inv[2], mean[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {  // added in the same order by all four
+    float a = 0.f, b = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 v = xch[(k * 2 + h) * 32 + lane];
+      a += v.x;
+      b += v.y;
+    }
+    inv[h] = rsqrtf(a * (1.0f / 128.0f) + p.eps_qk);
+    mean[h] = b * inv[h] * (1.0f / 128.0f);
+  }
+  bf16* dst = p.dqkv + (long)m * 3 * p.I + n0 + sub * 32;
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    float x[16], t[16], wv[16];
-    ld_chunk16(tb + c * 16, x);
-    unrotate16(d, valid, p3, freq, axis, c0 + c, t);
-    unpack16(w + (c0 + c) * 16, wv);
-    tmem_wait_ld();
-    if (c == 3) release();
+  for (int c = 0; c < 2; ++c) {
+    float cs[8], sn[8];
+    angles(c, cs, sn);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float xh = x[j] * inv;
-      x[j] = inv * (t[j] * wv[j] - xh * mean);
-      t[j] *= xh;
-    }
-    uint32_t out[8];
-    pack_row<16>(x, out);
-    store16(dst + c * 16, 3L * p.I, m, p.rows, out);
-    // sum over the warp's 32 rows: lanes 2l and 2l + 1 end with column l
+    for (int h = 0; h < 2; ++h) {
+      float x[16], t[16], wv[16];
+      ld_chunk16(tb + h * 128 + c * 16, x);
+      turn_back(d[h] + c * 16, cs, sn, t);
+      unpack16(w[h] + c * 16, wv);
+      tmem_wait_ld();
+      if (c == 1 && h == 1) release();
 #pragma unroll
-    for (int o = 16; o > 1; o >>= 1) {
-      const bool up = (lane & o) != 0;
-#pragma unroll
-      for (int i = 0; i < o / 2; ++i) {
-        const float send = up ? t[i] : t[i + o / 2], keep = up ? t[i + o / 2] : t[i];
-        t[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+      for (int j = 0; j < 16; ++j) {
+        const float xh = x[j] * inv[h];
+        x[j] = inv[h] * (t[j] * wv[j] - xh * mean[h]);
+        t[j] *= xh;
       }
+      uint32_t out[8];
+      pack_row<16>(x, out);
+      store16(dst + h * 128 + c * 16, 3L * p.I, m, p.rows, out);
+      // sum over the warp's 32 rows: lanes 2l and 2l + 1 end with column l
+#pragma unroll
+      for (int o = 16; o > 1; o >>= 1) {
+        const bool up = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < o / 2; ++i) {
+          const float send = up ? t[i] : t[i + o / 2], keep = up ? t[i + o / 2] : t[i];
+          t[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+      }
+      t[0] += __shfl_xor_sync(0xffffffffu, t[0], 1);
+      if ((lane & 1) == 0) wacc[part[h] * 32 + c * 16 + (lane >> 1)] += t[0];
     }
-    t[0] += __shfl_xor_sync(0xffffffffu, t[0], 1);
-    if ((lane & 1) == 0) wacc[c * 16 + (lane >> 1)] += t[0];
   }
   return true;
 }
@@ -377,7 +413,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 3);
   float* freq = reinterpret_cast<float*>(tmem_slot + 4);
   uint8_t* axis = reinterpret_cast<uint8_t*>(freq + 64);
-  uint64_t* xbar = reinterpret_cast<uint64_t*>(axis + 64);  // QKNORM: [8] two warps of a head row
+  uint64_t* xbar = reinterpret_cast<uint64_t*>(axis + 64);  // QKNORM: [4] the four warps of a lane quarter
   float* wacc = reinterpret_cast<float*>(smem + STAGES * STAGE + C::WTILE + C::MISC);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -397,7 +433,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
     mbar_init(drain, 1);
     mbar_init(w_full, 1);
     mbar_init(w_empty, EW);
-    for (int i = 0; i < 8; ++i) mbar_init(&xbar[i], 2);
+    for (int i = 0; i < 4; ++i) mbar_init(&xbar[i], 4);
     fence_mbar_init();
     for (int i = 0; i < p.n_maps; ++i) tma_prefetch_desc(&maps.m[i]);
   }
@@ -416,7 +452,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       freq[i] = powf(p.theta, -2.0f * (float)i_sec / (float)d_sec);
       axis[i] = (uint8_t)ax;
     }
-    for (int i = threadIdx.x; i < EW * 128; i += C::THREADS) wacc[i] = 0.f;
+    for (int i = threadIdx.x; i < EW * 64; i += C::THREADS) wacc[i] = 0.f;
   }
   tc_fence_before();
   __syncthreads();
@@ -590,12 +626,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         if (!wait_full()) break;
         epi_ffn(p, tmem_base + lane_off + (uint32_t)(acc * 256), m, w.nt, sub, release);
       } else if constexpr (KIND == QKNORM) {
-        if (!wait_full()) break;
-        // sub 0, 1 and 2, 3 share the tile's two heads
-        const int two = (sub >> 1) * 4 + q;
-        float2* xch = reinterpret_cast<float2*>(wacc + EW * 128) + (n_w & 1) * EW * 32 + two * 64;
-        ok = epi_qknorm(p, tmem_base + lane_off + (uint32_t)(acc * 256 + sub * COLS), m, w.nt * 256 + (sub >> 1) * 128,
-                        pr.N / 2, freq, axis, wacc + (warp - 2) * 128, xch, sub & 1, &xbar[two], n_w & 1, release);
+        float2* xch = reinterpret_cast<float2*>(wacc + EW * 64) + ((n_w & 1) * 4 + q) * 4 * 2 * 32;
+        ok = epi_qknorm(p, tmem_base + lane_off + (uint32_t)(acc * 256), m, w.nt * 256, pr.N / 2, sub, freq, axis,
+                        wacc + (warp - 2) * 64, xch, &xbar[q], n_w & 1, wait_full, release);
         if (!ok) break;
         ++n_w;
       } else if (pr.gated) {
@@ -675,12 +708,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
   tc_fence_before();
   __syncthreads();
   if constexpr (KIND == QKNORM) {
-    if (threadIdx.x < 256) {  // column c of q or k: the warps whose half of the head holds it
+    if (threadIdx.x < 256) {  // column c of q or k: the warps that hold it, one a lane quarter
       const int part = threadIdx.x >> 7, c = threadIdx.x & 127;
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < EW; ++w)
-        if (((w >> 2) & 1) == c >> 6) s += wacc[w * 128 + part * 64 + (c & 63)];
+      for (int k = 0; k < 4; ++k) s += wacc[((c >> 5) * 4 + k) * 64 + part * 32 + (c & 31)];
       p.w_part[(long)blockIdx.x * 256 + threadIdx.x] = s;
     }
   }
