@@ -1,9 +1,9 @@
 // tcgen05 GEMMs of the block's backward pass, all on CTA pairs (cta_group::2,
 // 256 x 256 output tiles over two SMs, fp32 accumulators in TMEM):
 //
-//   PRODUCTS  up to three independent products, the tiles of one after those of
-//           another in one persistent launch (one tail instead of three, and
-//           small ones side by side):
+//   PRODUCTS  up to three independent products; short ones in one persistent
+//           launch, the tiles of one after those of another (one tail instead
+//           of three, and small ones side by side):
 //     input gradient   out[t][n] = sum_k A[t][k] B[k][n].  B is the forward
 //           weight [out, in] read with its rows as the contraction, so no
 //           transposed copy of a weight exists: its tiles enter shared memory
@@ -890,10 +890,40 @@ struct Products {
       fin.reduce_cols = M;
     }
   }
+  // One launch for all products, or one for each: pairs that begin a product
+  // together walk it in step, so that a wave's shared panels are read from
+  // HBM once; those that run on into the next product while others finish the
+  // last lose that (QKV at 7,904 tokens: 6.1 against 4.7 GB read, and under
+  // the power cap 4.02 against 3.86 ms; out-projection at 32,160 tokens 4.53
+  // against 4.10 ms).  Short products gain more from the one tail and launch
+  // (out-projection at 4,096 tokens 532 against 567 us, 1,024 x 1,024 x 1,024
+  // 20 against 30 us).  The two meet near 2,000 k blocks for each pair.
+  bool together() const {
+    long blocks = 0;
+    for (int i = 0; i < p.n_products; ++i)
+      blocks += (long)p.pr[i].m_tiles * p.pr[i].n_tiles * (p.pr[i].kb[0] + p.pr[i].kb[1] + p.pr[i].kb[2]);
+    return blocks < 2000L * gemm_bwd::max_cta_pairs();
+  }
   cudaError_t run(cudaStream_t stream) {
     if (!good) return cudaErrorInvalidValue;
-    p.n_maps = n_maps;
-    const cudaError_t e = gemm_bwd::launch<gemm_bwd::PRODUCTS>(maps, p, stream);
+    cudaError_t e = cudaSuccess;
+    if (together()) {
+      p.n_maps = n_maps;
+      e = gemm_bwd::launch<gemm_bwd::PRODUCTS>(maps, p, stream);
+    } else {
+      for (int i = 0; i < p.n_products && e == cudaSuccess; ++i) {
+        gemm_bwd::Params one = p;
+        gemm_bwd::Maps m;
+        memset(&m, 0, sizeof(m));
+        one.pr[0] = p.pr[i];
+        one.n_products = 1;
+        one.n_maps = 2 * p.pr[i].segs + p.pr[i].gated;
+        memcpy(m.m, maps.m + p.pr[i].map0, one.n_maps * sizeof(CUtensorMap));
+        one.pr[0].map0 = 0;
+        one.gate_grad = p.gate_grad && p.pr[i].gated;
+        e = gemm_bwd::launch<gemm_bwd::PRODUCTS>(m, one, stream);
+      }
+    }
     return e != cudaSuccess ? e : launch_finish(fin, stream);
   }
 };
