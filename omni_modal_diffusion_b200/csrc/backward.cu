@@ -38,8 +38,8 @@ static AdalnPlan adaln_plan(int D) {
   const int nv = D / 4;
   if (nv <= 128) {
     // narrow rows: one warp a row, no barrier in its reductions, and as many
-    // of them as fit with four stages and 1.5 KB each (26,857 rows of 256:
-    // 49 us with a CTA of 64 threads a row, 29 us so)
+    // of them as fit with four stages and 1.5 KB each (26,857 rows of 256,
+    // the second launch included: 51 us with a CTA of 64 threads a row, 27 us so)
     p.vpt = (nv + 31) / 32;
     p.threads = 32;
     p.stages = AB_STAGES;
@@ -139,8 +139,9 @@ __global__ void __launch_bounds__(AB_MAX_THREADS, VPT <= 3 ? 2 : 1) adaln_bwd_ke
     bulk_load(dst + 4u * D, dres + (row0 + i) * D, 4u * D, &full[st]);
     bulk_load(dst + 8u * D, dy + (row0 + i) * D, 2u * D, &full[st]);
   };
+  int issued = 0;  // thread 0's
   if (threadIdx.x == 0)
-    for (int i = 0; i < stages - 1 && i < n_rows; ++i) load_row(i);
+    while (issued < stages - 1 && issued < n_rows) load_row(issued++);
   const float4* scale = reinterpret_cast<const float4*>(mod + (long)(m * 6 + 3 * branch + 1) * D);
   uint64_t a_shift[VPT][2], a_scale[VPT][2], sc[VPT][2];
 #pragma unroll
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(AB_MAX_THREADS, VPT <= 3 ? 2 : 1) adaln_bwd_ke
     }
     block_sums<1>(s1, red[0]);
     // every thread has left row r - 1, whose stage takes row r + stages - 1
-    if (threadIdx.x == 0 && r + stages - 1 < n_rows) load_row(r + stages - 1);
+    if (threadIdx.x == 0 && r + stages - 1 < n_rows) load_row(issued++);
     const float mu = s1[0] / (float)D;  // divided as the forward call divides: a constant row has xhat = 0
     const uint64_t nmu = f2_pack(-mu, -mu);
     uint64_t q[3] = {0ull, 0ull, 0ull};  // sum (x - mu)^2, sum dh, sum dh (x - mu)
@@ -220,6 +221,7 @@ __global__ void __launch_bounds__(AB_MAX_THREADS, VPT <= 3 ? 2 : 1) adaln_bwd_ke
       }
     }
   }
+  if (threadIdx.x == 0 && !ok) drain_loads(full, stages, issued);  // after a wait that gave up
   ulonglong2* p0 = reinterpret_cast<ulonglong2*>(part + (long)blockIdx.x * 2 * D);
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {

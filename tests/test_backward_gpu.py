@@ -599,6 +599,98 @@ def test_two_streams_at_once():
         assert torch.equal(gx, ax) and torch.equal(gdx, adx) and all(torch.equal(g[n], ag[n]) for n in ag)
 
 
+def test_captured_behind_copies_memsets_and_another_stream():
+    """Each call captured right behind a memory copy, a memset and a join with
+    a second stream that fills its inputs: replays give the eager call's bits
+    (no kernel of a chain starts on inputs that are not there yet)."""
+    t = Inputs((37, 58, 1900), 576, 6, 1280, seed=113, fill=0.0)
+    mod, pos = dev(t.normal(3, 6, t.D, std=0.3), F32), t.rows(t.rng.integers(0, 20, (t.L, 3)), F32)
+    W = {n: dev(t.normal(*s, std=0.05)) for n, s in (("qkv", (3 * t.I, t.D)), ("o", (t.D, t.I)), ("gu", (2 * t.F, t.D)),
+                                                     ("d", (t.D, t.F)))}
+    w = dev(t.normal(128, std=0.1, mean=1.0))
+    src = {n: f(t.normal(*s)) for n, s, f in (
+        ("xm", (t.L, t.D), t.rows), ("o", (t.L, t.I), t.rows), ("do", (t.L, t.I), t.rows),
+        ("q", (t.L, t.H, 128), t.heads), ("k", (t.L, t.H, 128), t.heads), ("v", (t.L, t.H, 128), t.heads))}
+    src |= {n: t.rows(t.normal(t.L, t.D), F32) for n in ("x", "dx")}
+    src["lse"] = torch.full((t.H, t.Lp), 9.0, device=DEV)
+    buf = {n: torch.zeros_like(a) for n, a in src.items()}
+    ws = {op: t.ws(op) for op in range(5)}
+    e = lambda *s, dt=BF16: torch.zeros(*s, dtype=dt, device=DEV)  # noqa: E731
+
+    def outputs(make):
+        def of(fn):
+            fn.outputs = make
+            return fn
+        return of
+
+    @outputs(lambda: (e(t.Lp, t.D, dt=F32), e(3, 6, t.D)))
+    def adaln(b, stream, out):
+        h3.h3_adaln_norm_modulate_backward(t.dims, t.ranges, b["x"], mod, 0, b["xm"], b["dx"], *out, ws[0], stream)
+
+    @outputs(lambda: (e(t.Lp, t.D), e(3 * t.I, t.D), e(128), e(128)))
+    def qkv(b, stream, out):
+        h3.h3_qkv_qknorm_mrope_backward(t.dims, t.ranges, b["xm"], W["qkv"], w, w, pos, b["q"], b["k"], b["v"], *out,
+                                        ws[1], stream)
+
+    @outputs(lambda: tuple(e(t.H, t.Lp, 128) for _ in range(3)))
+    def attention(b, stream, out):
+        h3.h3_attention_backward(t.dims, t.ranges, b["q"], b["k"], b["v"], b["o"], b["lse"], b["do"], *out, ws[2],
+                                 stream)
+
+    @outputs(lambda: (e(t.Lp, t.I), e(t.D, t.I), e(3, 6, t.D)))
+    def gated(b, stream, out):
+        h3.h3_gated_residual_backward(t.dims, t.ranges, b["dx"], b["o"], W["o"], mod, *out, ws[3], stream=stream)
+
+    @outputs(lambda: (e(t.Lp, t.D), e(2 * t.F, t.D), e(t.D, t.F), e(3, 6, t.D)))
+    def ffn(b, stream, out):
+        h3.h3_ffn_swiglu_backward(t.dims, t.ranges, b["dx"], b["xm"], W["gu"], W["d"], mod, *out, ws[4], stream)
+
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    for call in (adaln, qkv, attention, gated, ffn):
+        want = call.outputs()
+        call(src, None, want)
+        torch.cuda.synchronize()
+        for kind in ("copy", "memset", "join"):
+            for b in buf.values():
+                b.zero_()
+            torch.cuda.synchronize()
+            got, graph = call.outputs(), torch.cuda.CUDAGraph()  # outputs first: the call follows the copies
+            with torch.cuda.graph(graph, stream=main):
+                if kind == "join":
+                    side.wait_stream(main)
+                    with torch.cuda.stream(side):
+                        for n in buf:
+                            buf[n].copy_(src[n])
+                    main.wait_stream(side)
+                    call(buf, main, got)
+                else:
+                    for n in buf:
+                        if kind == "memset":
+                            buf[n].zero_()
+                        else:
+                            buf[n].copy_(src[n])
+                    call(buf, main, got)
+            for _ in range(2):
+                for b in buf.values():
+                    b.fill_(3.0)
+                for g in got:
+                    g.fill_(1.0)
+                torch.cuda.synchronize()
+                graph.replay()
+                torch.cuda.synchronize()
+                same = want
+                if kind == "memset":
+                    same = call.outputs()
+                    call(buf, None, same)
+                    torch.cuda.synchronize()
+                for g, r in zip(got, same):
+                    if g.shape == (3, 6, t.D):  # slots that are not the call's hold what stood there
+                        mine = (r != 0).any(-1)
+                        g, r = g[mine], r[mine]
+                    assert torch.equal(g, r), (call.__name__, kind)
+    t.finish()
+
+
 # ---------------------------------------------------------------- refusals
 
 def test_python_forms_check_sizes_types_and_workspace():
