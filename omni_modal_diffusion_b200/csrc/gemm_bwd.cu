@@ -53,12 +53,14 @@ struct Product {
   // The contraction in `splits` equal runs of k blocks, each a unit of work of
   // its own that writes an fp32 partial, part [splits][M][N]; 1: none
   int splits, units;
+  int per;            // k blocks of a split
   float* part;
   bf16* out;          // [M][N]; null (gated only): not wanted
 };
 
 struct Params {
   int n_products, units, n_maps;
+  int catch_up;       // units after the first product's for the pairs that its last turn leaves out
   Product pr[MAX_PRODUCTS];
   // the gated product
   const float* mod;   // [3][6][D], D = its M
@@ -119,6 +121,13 @@ __device__ __forceinline__ void ld_chunk16(uint32_t taddr, float* v) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+// 32 lanes x 8 consecutive 32-bit columns
+__device__ __forceinline__ void ld_chunk8(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
 }
 // (L1::no_allocate: what is left of L1 beside the stages serves the loads; 9%
 // of a weight gradient over 64 tokens, which is bound by its stores)
@@ -380,15 +389,30 @@ __device__ __forceinline__ Unit unit_of(const Params& p, int u) {
   tile_coords(u - w.sp * tiles, pr.m_tiles, pr.n_tiles, pr.group_m, w.mt, w.nt);
   return w;
 }
+// The pair's unit after u (its first: after pair - n_pairs): the first
+// product's in turns of all pairs, then the catch_up units in turns of the
+// pairs without one in its last, partial turn, then the rest in turns of all,
+// those pairs first.
+template <int KIND>
+__device__ __forceinline__ int next_unit(const Params& p, int u, int pair, int n_pairs) {
+  if constexpr (KIND != PRODUCTS) return u + n_pairs;
+  const int n0 = p.pr[0].units, end = n0 + p.catch_up, rem = n0 % n_pairs;
+  if (u < n0) {
+    u += n_pairs;
+    if (u < n0) return u;
+    u = pair < rem ? end : n0 + pair - rem;
+  } else if (u < end) {
+    u += n_pairs - rem;
+  } else {
+    return u + n_pairs;
+  }
+  return u < end ? u : end + n_pairs - 1 - pair;
+}
 // k blocks [lo, hi) of segment sg in split sp, the segments' blocks counted one
 // after another
 __device__ __forceinline__ void seg_range(const Product& pr, int sp, int sg, int& lo, int& hi) {
-  int total = pr.kb[0], before = 0;
-  if (pr.segs > 1) {
-    total += pr.kb[1] + pr.kb[2];
-    before = sg == 0 ? 0 : (sg == 1 ? pr.kb[0] : pr.kb[0] + pr.kb[1]);
-  }
-  const int per = (total + pr.splits - 1) / pr.splits, n = pr.kb[sg];
+  const int before = sg == 0 ? 0 : (sg == 1 ? pr.kb[0] : pr.kb[0] + pr.kb[1]);
+  const int per = pr.per, n = pr.kb[sg];
   lo = min(n, max(0, sp * per - before));
   hi = max(lo, min(n, (sp + 1) * per - before));
 }
@@ -468,7 +492,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       uint32_t phase = 0;
       long long issued = 0;
       bool ok = true;
-      for (int u = pair; u < p.units && ok; u += n_pairs) {
+      for (int u = next_unit<KIND>(p, pair - n_pairs, pair, n_pairs); u < p.units && ok;
+           u = next_unit<KIND>(p, u, pair, n_pairs)) {
         // One thread feeds the tile: everything its loop needs is in registers
         // before it (a parameter indexed by the product costs the whole kernel
         // 7% when it is read again for every load).
@@ -535,7 +560,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
-      for (int u = pair; u < p.units && ok; u += n_pairs) {
+      for (int u = next_unit<KIND>(p, pair - n_pairs, pair, n_pairs); u < p.units && ok;
+           u = next_unit<KIND>(p, u, pair, n_pairs)) {
         const Unit w = unit_of<KIND>(p, u);
         const Product& pr = p.pr[w.product];
         // the MMAs' descriptors are constants but for the start address: one
@@ -585,7 +611,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
   } else if (warp >= 2 + EW) {  // PRODUCTS: the gated product's tiles of W
     if (lane == 0 && p.gate_grad) {
       int n = 0;
-      for (int u = pair; u < p.units; u += n_pairs) {
+      for (int u = next_unit<KIND>(p, pair - n_pairs, pair, n_pairs); u < p.units;
+         u = next_unit<KIND>(p, u, pair, n_pairs)) {
         const Unit w = unit_of<KIND>(p, u);
         const Product& pr = p.pr[w.product];
         if (!pr.gated) continue;
@@ -617,7 +644,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
     };
     const uint32_t lane_off = (uint32_t)(q * 32) << 16;
     int n_w = 0;
-    for (int u = pair; u < p.units; u += n_pairs) {
+    for (int u = next_unit<KIND>(p, pair - n_pairs, pair, n_pairs); u < p.units;
+         u = next_unit<KIND>(p, u, pair, n_pairs)) {
       const Unit w = unit_of<KIND>(p, u);
       const Product& pr = p.pr[w.product];
       const int m = w.mt * 256 + (int)rank * 128 + row_in_tile;
@@ -657,23 +685,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
           const float gate = in ? __ldg(p.mod + (long)(sg * 6 + p.gate_slot) * pr.M + m) : 0.f;
           if (!wait_full()) break;
           const uint32_t tb = tmem_base + lane_off + (uint32_t)(acc * 256 + sub * COLS);
+          // eight columns at a time: with 16 more of the sums spill (out-projection
+          // at 512 tokens 87.6 us, so 85.7; at 2,048 tokens 262 and 258)
           float dot = 0.f;
 #pragma unroll
-          for (int c = 0; c < COLS; c += 16) {
-            float v[16];
-            ld_chunk16(tb + c, v);
+          for (int c = 0; c < COLS; c += 8) {
+            float v[8];
+            ld_chunk8(tb + c, v);
             tmem_wait_ld();
             if (p.gate_grad) {
+              float wv[8];
+              unpack8(*reinterpret_cast<const uint4*>(wrow + (((c >> 3) ^ (row_in_tile & 7)) << 4)), wv);
 #pragma unroll
-              for (int j = 0; j < 16; j += 8) {
-                float wv[8];
-                unpack8(*reinterpret_cast<const uint4*>(wrow + ((((c + j) >> 3) ^ (row_in_tile & 7)) << 4)), wv);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) dot = fmaf(wv[i], v[j + i], dot);
-              }
+              for (int i = 0; i < 8; ++i) dot = fmaf(wv[i], v[i], dot);
             }
 #pragma unroll
-            for (int j = 0; j < 16; ++j) sum[c + j] = fmaf(gate, v[j], sum[c + j]);
+            for (int j = 0; j < 8; ++j) sum[c + j] = fmaf(gate, v[j], sum[c + j]);
           }
           release();
           if (p.gate_grad && in) *gp = dot;
@@ -785,6 +812,31 @@ void set_tiles(Product& pr, int M, int N, int n_step) {
   pr.group_m = pr.m_tiles < 8 ? pr.m_tiles : 8;
 }
 
+// What the pairs that the first product's last turn leaves out do meanwhile, in
+// units of the products after it.  A unit takes its k blocks' time, or where
+// they are few its epilogue's (24 k blocks with a gate, 12 without).  Measured
+// with and without: out-projection at full width, 512 tokens (56 units of 84 k
+// blocks, then 588 of 8) 87.8 and 90.8 us, 352 tokens 105.8 and 111.9, 2,048
+// tokens 263 and 269.  (Costs of 16 and 40 for 24: 87.8 and 91.6, 113.7 and 112.8.)
+int catch_up_units(const Params& p, int pairs) {
+  auto cost = [&](const Product& pr) {
+    const int kb = (pr.kb[0] + pr.kb[1] + pr.kb[2] + pr.splits - 1) / pr.splits, least = pr.gated ? 24 : 12;
+    return kb > least ? kb : least;
+  };
+  const int rem = p.pr[0].units % pairs, light = pairs - rem;
+  if (p.n_products < 2 || rem == 0) return 0;
+  int spare = cost(p.pr[0]), rounds = 0, rest = 0;
+  for (int i = 1; i < p.n_products; ++i) rest += p.pr[i].units;
+  for (int i = 1; i < p.n_products; ++i) {
+    const int c = cost(p.pr[i]), all = (p.pr[i].units + light - 1) / light;
+    const int n = all < spare / c ? all : spare / c;
+    rounds += n;
+    spare -= n * c;
+    if (n < all) break;
+  }
+  return rounds * light < rest ? rounds * light : rest;
+}
+
 template <int KIND>
 cudaError_t launch(const Maps& maps, Params& p, cudaStream_t stream) {
   static unsigned long long attr_done = 0;
@@ -795,10 +847,12 @@ cudaError_t launch(const Maps& maps, Params& p, cudaStream_t stream) {
   for (int i = 0; i < p.n_products; ++i) {
     Product& pr = p.pr[i];
     pr.units = pr.m_tiles * pr.n_tiles * pr.splits;
+    pr.per = (pr.kb[0] + pr.kb[1] + pr.kb[2] + pr.splits - 1) / pr.splits;
     p.units += pr.units;
   }
   const int max_pairs = max_cta_pairs();
   const int pairs = p.units < max_pairs ? p.units : max_pairs;
+  p.catch_up = catch_up_units(p, pairs);
   return launch_chained(gemm_bwd_kernel<KIND>, dim3(2 * pairs), Cfg<KIND>::THREADS, Cfg<KIND>::BYTES, stream, maps, p);
 }
 
