@@ -24,6 +24,14 @@
 //   FFN       gate, up = A Wgu^T and dh = dY Wd in one K loop, and in the
 //           epilogue h = SiLU(g) u and the gradients of g and u.
 //
+// Tensor cores bound all three where contractions are long.  Tensor pipe active
+// at 2,048 tokens of width 5,376 (56 heads, F 14,336): QKNORM 87% (231 us), FFN
+// 90% (660 us), input and weight gradients 92-97%.  A gated weight gradient
+// over short modality ranges has an epilogue for each (57% there, 29 k blocks
+// the longest), and over 512 tokens (8 k blocks a tile) its stores and the tiles
+// of W bound it.  Long calls run against the power limit: 1,250-1,300 TFLOP/s
+// sustained.
+//
 // A segment, a ragged length and the padding rows end inside a tile: the tensor
 // maps stop at the last valid token, and TMA reads zeros past it.
 #include "h3_internal.cuh"
@@ -97,8 +105,8 @@ struct Cfg {
   // TMEM and global accesses of one tile.
   static constexpr int EW = 16;
   // PRODUCTS: one more warp loads the tile of W that a gate's gradient needs.
-  // (Five stages beside its 64 KB: 2-4% faster than four for the gated
-  // product, and as fast as six for the others.)
+  // (Five stages beside its 64 KB: 2-4% faster than four for the gated product,
+  // 1% slower than six for a long input gradient.)
   static constexpr int THREADS = (2 + EW + (KIND == PRODUCTS ? 1 : 0)) * 32;
   static constexpr int WTILE = KIND == PRODUCTS ? 4 * OPERAND : 0;  // 128 rows x 256 columns
   static constexpr int MISC = 768;
