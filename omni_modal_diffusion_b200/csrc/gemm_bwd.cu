@@ -25,9 +25,10 @@
 //           epilogue h = SiLU(g) u and the gradients of g and u.
 //
 // Tensor cores bound all three where contractions are long.  Tensor pipe active
-// at 2,048 tokens of width 5,376 (56 heads, F 14,336): QKNORM 87% (231 us), FFN
-// 90% (660 us), input and weight gradients 92-97%.  A gated weight gradient
-// over short modality ranges has an epilogue for each (57% there, 29 k blocks
+// while an SM has tiles, at 2,048 tokens of width 5,376 (56 heads, F 14,336):
+// QKNORM 86% (235 us), FFN 89% (676 us), input and weight gradients 95-97%.  A
+// gated weight gradient over short modality ranges has an epilogue for each
+// range (59% there, 29 k blocks
 // the longest), and over 512 tokens (8 k blocks a tile) its stores and the tiles
 // of W bound it.  Long calls run against the power limit: 1,250-1,300 TFLOP/s
 // sustained.
@@ -344,7 +345,10 @@ __device__ __forceinline__ bool epi_qknorm(const Params& p, uint32_t tb, int m, 
 
 // h = SiLU(g) u, du = dh SiLU(g), dg = dh u sig(g) (1 + g (1 - sig(g))) for 32 of
 // the tile's 128 hidden columns; accumulator columns [0, 128) g, [128, 256) u,
-// [256, 384) dh
+// [256, 384) dh.  h, dg and du are rounded to bf16 (half a step, 2^-8 at most),
+// as operands of the products that follow; with the gradient's own operand and
+// the result that makes 2.9e-3 of a result's 2-norm, 1.7e-3 of it the result's
+// rounding.  A second bf16 for what each loses would cost a quarter more time.
 template <typename Release>
 __device__ __forceinline__ void epi_ffn(const Params& p, uint32_t tb, int m, int nt, int sub, Release release) {
   uint32_t hw[16], gw[16], uw[16];
