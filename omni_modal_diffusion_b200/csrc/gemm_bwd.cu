@@ -28,9 +28,8 @@
 // while an SM has tiles, at 2,048 tokens of width 5,376 (56 heads, F 14,336):
 // QKNORM 86% (235 us), FFN 89% (676 us), input and weight gradients 95-97%.  A
 // gated weight gradient over short modality ranges has an epilogue for each
-// range (59% there, 29 k blocks
-// the longest), and over 512 tokens (8 k blocks a tile) its stores and the tiles
-// of W bound it.  Long calls run against the power limit: 1,250-1,300 TFLOP/s
+// range (59% there, 29 k blocks the longest), and over 512 tokens (8 k blocks a
+// tile) its stores and the tiles of W bound it.  Long calls run against the power limit: 1,250-1,300 TFLOP/s
 // sustained.
 //
 // A segment, a ragged length and the padding rows end inside a tile: the tensor
