@@ -326,6 +326,16 @@ def test_ffn_saturated_gates():
         inside(got, w, name)
 
 
+@pytest.mark.parametrize("counts,widths", (((40, 0, 260), (1024, 16, 4096)), ((100, 33, 200), (2048, 16, 2048)),
+                                           ((0, 513, 7), (1984, 15, 1920))), ids=str)
+def test_products_over_several_turns(counts, widths):
+    """More output tiles than the GPU has CTA pairs, in one launch: pairs that
+    the first product's last turn leaves out go on with the next product's."""
+    test_qkv(counts, widths, 0)
+    test_gated_residual(counts, widths, 0, h3.H3_MSA)
+    test_ffn(counts, widths, 1)
+
+
 # ---------------------------------------------------------------- long sequences
 
 LONG = (512, 1200, 122304)  # the packed 15 s sequence: 124,016 tokens
