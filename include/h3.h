@@ -590,7 +590,9 @@ int h3_attention_lse(const h3_dims* dims, const h3_ranges* ranges, const h3_bf16
 
 /* Backward of h3_attention_lse (same q, k, v; its o and lse): from d_o, the
  * gradient of o [L_pad][H*128], the gradients dq, dk, dv [H][L_pad][128] bf16.
- * The probabilities are recomputed from lse. */
+ * The probabilities are recomputed from lse, and each row's sum of P (.) dP with
+ * them: o gives a first estimate of it only, so that what o's rounding to bf16
+ * lost does not reach the gradients. */
 int h3_attention_backward(const h3_dims* dims, const h3_ranges* ranges, const h3_bf16* q, const h3_bf16* k,
                           const h3_bf16* v, const h3_bf16* o, const float* lse, const h3_bf16* d_o, h3_bf16* dq,
                           h3_bf16* dk, h3_bf16* dv, void* ws, void* stream);

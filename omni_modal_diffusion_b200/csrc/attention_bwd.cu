@@ -5,28 +5,39 @@
 //   dQ = c dS K,  dK = c dS^T Q.
 // The probabilities are recomputed, never stored.
 //
-// Two passes instead of one: a CTA owns a key tile and walks the queries (dK,
-// dV) or a query tile and walks the keys (dQ).  S and dP are taken twice, seven
-// tile products instead of five, but each result then lives in one CTA's TMEM:
-// no fp32 dQ in memory, no atomics (the same call gives the same bits), and P^T
-// and dS go from the registers that computed them to TMEM as the next product's
-// A operand.  One
-// kernel with five products has to turn dS through shared memory and add a
-// 64 KB dQ tile per step to memory: 256 KB of MMA operands, 32 KB of dS and
-// 128 KB of dQ through the 128 B/clk of shared memory are 3,300 clocks a tile
-// pair, against 3,584 clocks of tensor time for the seven.
+// Two passes instead of one: a CTA owns a query tile and walks the keys (dQ), or
+// a key tile and walks the queries (dK, dV).  S and dP are taken twice, but each
+// result then lives in one CTA's TMEM: no fp32 dQ in memory, no atomics (the
+// same call gives the same bits), and P and dS go from the registers that
+// computed them to TMEM as the next product's A operand.
 //
-// Measured: 56 heads of 7,904 tokens 4.85 ms, 4 heads of 32,160 tokens 5.47 ms:
-// 923 and 968 TFLOP/s counting five products, 1,290 and 1,355 of the seven done.
-// The tensor cores bound it (75% of the cycles active, and the SM clock at some
-// 1.3 of 1.9 GHz under the power limit).
+// delta cannot be had from O alone: O is bf16, and a row whose delta is off by e
+// has e P_ij in every dS_ij, so e times the mean key in dQ, where dS K itself
+// lets everything that the keys share drop out.  (Unit-variance keys and values
+// with an offset of the same size in each channel: dQ off by 3.5e-2 of its
+// 2-norm at 1,024 tokens, 8e-2 at 4,096; offsets of 4: 0.76.)  The rows of dS
+// sum to 0 with the delta of P and dP themselves, so the query tiles start from
+// delta(O), take rho = rowsum(dS) in fp32 and, beside dS K, P K, and end with
+//   dQ = c (dS K - rho P K),  delta = delta(O) + rho,
+// the second for the key tiles, which come after.  rho is some 2^-8 of dS's
+// terms, so the rounding of P in P K does not matter.  That makes eight tile
+// products of the five that the formulas have, and two launches that follow one
+// another.
 //
-// P and dS are rounded to bf16 for their products (half a step, relative 2^-8 at most, each,
-// as the forward pass rounds P); sums, exponentials and the subtraction are fp32.
+// Measured: 56 heads of 7,904 tokens 5.5 ms, 4 heads of 32,160 tokens 6.2 ms:
+// 814 and 855 TFLOP/s counting five products, 1,300 and 1,370 of the eight done,
+// at the power limit.  (With delta from O alone, seven products in one launch:
+// 4.9 and 5.4 ms; 64 tokens, 4 heads: 14 us, so 22.)
+//
+// P and dS are rounded to bf16 for their products (half a step, relative 2^-8 at
+// most, each, as the forward pass rounds P); sums, exponentials and the
+// subtraction are fp32.
 //
 // Valid rows end inside a tile: the tensor maps stop at token L, TMA reads
-// zeros past it (whatever the padding rows hold), masked queries have
-// lse = +inf (P = 0), and masked keys are set to P = 0 in the last key tile.
+// zeros past it (whatever the padding rows hold), and masked queries have
+// lse = +inf (P = 0).  Masked keys are set to P = 0 in the last key tile that a
+// query tile walks; in a key tile they are rows of their own, zeroed as they are
+// stored.
 #include "h3_internal.cuh"
 #include "ptx.cuh"
 
@@ -42,39 +53,6 @@ using attn_split::tmem_st16;
 // tile's 128 columns
 constexpr int THREADS = 18 * 32;
 constexpr int CWARPS = 16;
-
-// ------------------------------------------------------------ row statistics
-// nlse2[h][r] = -lse log2(e) (-inf past L: P = 0), ndelta[h][r] = -sum_d do o
-// (0 past L).  16 threads per (row, head), 8 elements each.
-__global__ void __launch_bounds__(256) attention_delta_kernel(const bf16* __restrict__ o, const bf16* __restrict__ d,
-                                                              const float* __restrict__ lse, int H, int L, int L_pad,
-                                                              float* __restrict__ nlse2, float* __restrict__ ndelta) {
-  const long total = (long)L_pad * H * 16;
-  chain_wait();
-  for (long i = blockIdx.x * 256L + threadIdx.x; i < total; i += gridDim.x * 256L) {
-    const long rh = i >> 4;
-    const int row = (int)(rh / H), h = (int)(rh - (long)row * H);
-    float s = 0.f;
-    if (row < L) {
-      const uint4 a = __ldcs(reinterpret_cast<const uint4*>(o) + i), b = __ldcs(reinterpret_cast<const uint4*>(d) + i);
-      const __nv_bfloat162 *pa = reinterpret_cast<const __nv_bfloat162*>(&a),
-                           *pb = reinterpret_cast<const __nv_bfloat162*>(&b);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 x = __bfloat1622float2(pa[j]), y = __bfloat1622float2(pb[j]);
-        s = fmaf(x.x, y.x, s);
-        s = fmaf(x.y, y.y, s);
-      }
-    }
-#pragma unroll
-    for (int k = 8; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-    if ((threadIdx.x & 15) == 0) {
-      const long at = (long)h * L_pad + row;
-      ndelta[at] = -s;
-      nlse2[at] = row < L ? -lse[at] * 1.4426950408889634f : -INFINITY;
-    }
-  }
-}
 
 struct BwdMaps {
   CUtensorMap q, k, v;  // [H][L][128] (row stride 128, head stride L_pad * 128)
@@ -157,8 +135,9 @@ __device__ __forceinline__ void zero_cols32(bf16* dst) {
 // each) over it, dV, dK.  S^T(i) is free as soon as it is in registers, so the
 // next one is taken while its exponentials run, and the tensor core's turn is
 //   dV(i) dK(i) dP^T(i + 1) S^T(i + 2)
-// of which only dV waits for the elementwise warps: P^T(i) is stored the
-// moment dP^T(i) has been read, while S^T(i + 1), already issued, runs.
+// where dV waits for P^T(i), which is stored the moment dP^T(i) has been read,
+// while S^T(i + 1), already issued, runs; dK for dS^T(i); and S^T(i + 2) for
+// S^T(i + 1) to be in registers.
 struct KvLayout {
   static constexpr int QS = 3;  // Q stages: Q(i + 2) for S^T(i + 2) is loaded while dK(i) still reads Q(i)
   static constexpr int K = 0, V = TILE_BYTES, Q = 2 * TILE_BYTES, D = Q + QS * TILE_BYTES;  // dO: two stages
@@ -169,8 +148,11 @@ struct KvLayout {
 };
 
 struct BwdArgs {
-  const bf16 *q, *d;
-  const float *nlse2, *ndelta;
+  const bf16 *o, *d;  // [L_pad][H * 128]
+  const float* lse;   // [H][L_pad]
+  // Row statistics [H][L_pad], which the query tiles leave for the key tiles:
+  // -lse log2(e) (-inf past L: P = 0) and -delta (0 past L)
+  float *nlse2, *ndelta;
   int H, L, L_pad;
   float scale, scale_log2;
   bf16 *dq, *dk, *dv;
@@ -408,50 +390,40 @@ __device__ __forceinline__ void key_tile(const BwdMaps& maps, const BwdArgs& p, 
 }
 
 // ------------------------------------------------------------ dQ
-// TMEM: S(j) [0, 128), dP(j) [128, 256) with dS(j) over it, dQ [256, 384), and
-// Q and dO as bf16 A operands, [384, 448) and [448, 512): with both operands
-// in shared memory S and dP would read 128 KB of it a tile, with dQ's 32 KB and
-// the 64 KB that TMA writes 1,792 of its clocks against 1,536 of the tensor
-// core's.  As in the other kernel S(j) is free once it is in registers:
-//   dQ(j) dP(j + 1) S(j + 2)
-// of which dQ waits for dS(j).
+// The same pipeline on a query tile: TMEM S(j) [0, 128), dP(j) [128, 256) with P
+// and dS (bf16) over it, the running dS K [256, 384) and P K [384, 512).  Both
+// read K(j) and P(j) or dS(j):
+//   PK(j) dSK(j) dP(j + 1) S(j + 2)
+// with the waits of the key tiles.  K has three stages, as Q has there.
 struct QLayout {
-  static constexpr int KS = 4, VS = 2;  // K stages: K(j) for dQ(j) while S(j + 2) reads K(j + 2)
-  static constexpr int K = 0, V = KS * TILE_BYTES;
-  static constexpr int BAR = V + VS * TILE_BYTES;
+  static constexpr int KS = 3, VS = 2;
+  static constexpr int Q = 0, D = TILE_BYTES, K = 2 * TILE_BYTES, V = K + KS * TILE_BYTES;
+  static constexpr int SUM = V + VS * TILE_BYTES;  // [4 column groups][128 rows] sums of do o, then of dS
+  static constexpr int BAR = SUM + 4 * 128 * 4;
   static constexpr int BYTES = BAR + 256;
-  static_assert(BYTES <= KvLayout::BYTES, "shared memory per CTA");
+  static_assert(BYTES <= 232448, "shared memory per CTA");
 };
 
-// D = A B^T over d = 128: A bf16 in TMEM, B a K-major 128 x 128 tile
-__device__ __forceinline__ void mma_tmem_abt(uint32_t d_tmem, uint32_t a_tmem, uint64_t bd) {
-  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false);
-#pragma unroll
-  for (int kk = 0; kk < 8; ++kk)
-    umma_bf16_tmem_a(d_tmem, a_tmem + kk * 8, bd + (uint64_t)(((kk >> 2) * HALF_BYTES + (kk & 3) * 32) >> 4), idesc,
-                     kk != 0 ? 1u : 0u);
-}
-
 __device__ __forceinline__ void query_tile(const BwdMaps& maps, const BwdArgs& p, int tile, int h, uint8_t* smem) {
-  const bf16 *q = p.q, *d = p.d;
   const int L = p.L, L_pad = p.L_pad, H = p.H;
   const float scale = p.scale, scale_log2 = p.scale_log2;
   bf16* dq = p.dq;
   using Y = QLayout;
   constexpr int KS = Y::KS, VS = Y::VS;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Y::BAR);
-  uint64_t* q_ready = bars + 0;      // Q and dO in TMEM
+  uint64_t* qd_full = bars + 0;
   uint64_t* k_full = bars + 1;       // [KS]
-  uint64_t* k_empty = k_full + KS;   // [KS] after dQ of the tile
+  uint64_t* k_empty = k_full + KS;   // [KS] after dS K of the tile
   uint64_t* v_full = k_empty + KS;   // [VS]
   uint64_t* v_empty = v_full + VS;   // [VS] after dP of the tile
   uint64_t* s_full = v_empty + VS;
-  uint64_t* s_read = s_full + 1;
+  uint64_t* s_read = s_full + 1;     // S in registers
   uint64_t* dp_full = s_full + 2;
-  uint64_t* ds_ready = s_full + 3;
-  uint64_t* acc_full = s_full + 4;
-  uint64_t* drain = s_full + 5;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 6);
+  uint64_t* p_ready = s_full + 3;
+  uint64_t* ds_ready = s_full + 4;
+  uint64_t* acc_full = s_full + 5;
+  uint64_t* drain = s_full + 6;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 7);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int row0 = tile * TILE;
   const int n_k = (L + TILE - 1) / TILE;
@@ -461,7 +433,7 @@ __device__ __forceinline__ void query_tile(const BwdMaps& maps, const BwdArgs& p
     return;
   }
   if (threadIdx.x == 0) {
-    mbar_init(q_ready, CWARPS);
+    mbar_init(qd_full, 1);
     for (int s = 0; s < KS; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
@@ -473,6 +445,7 @@ __device__ __forceinline__ void query_tile(const BwdMaps& maps, const BwdArgs& p
     mbar_init(s_full, 1);
     mbar_init(s_read, CWARPS);
     mbar_init(dp_full, 1);
+    mbar_init(p_ready, CWARPS);
     mbar_init(ds_ready, CWARPS);
     mbar_init(acc_full, 1);
     mbar_init(drain, 1);
@@ -491,6 +464,9 @@ __device__ __forceinline__ void query_tile(const BwdMaps& maps, const BwdArgs& p
 
   if (warp == 0) {
     if (lane == 0) {
+      mbar_arrive_expect_tx(qd_full, 2 * TILE_BYTES);
+      load_head_tile(smem + Y::Q, &maps.q, qd_full, row0, h);
+      load_token_tile(smem + Y::D, &maps.d, qd_full, row0, h);
       long long k_issued = 0, v_issued = 0;
       for (int j = 0; j < n_k; ++j) {
         const int sk = j % KS, sv = j % VS;
@@ -503,10 +479,13 @@ __device__ __forceinline__ void query_tile(const BwdMaps& maps, const BwdArgs& p
         load_head_tile(smem + Y::V + sv * TILE_BYTES, &maps.v, &v_full[sv], j * TILE, h);
         ++v_issued;
       }
+      mbar_wait(qd_full, 0);
       drain_loads(k_full, KS, k_issued);
       drain_loads(v_full, VS, v_issued);
     }
   } else if (warp == 1) {
+    const uint64_t qd = sdesc_sw128(smem_u32(smem + Y::Q), 16, 1024);
+    const uint64_t dd = sdesc_sw128(smem_u32(smem + Y::D), 16, 1024);
     const uint64_t kd = sdesc_sw128(smem_u32(smem + Y::K), 16, 1024);
     const uint64_t vd = sdesc_sw128(smem_u32(smem + Y::V), 16, 1024);
     const uint64_t kd_mn = sdesc_sw128(smem_u32(smem + Y::K), HALF_BYTES, 1024);
@@ -515,23 +494,26 @@ __device__ __forceinline__ void query_tile(const BwdMaps& maps, const BwdArgs& p
       if (!mbar_wait_warp(&k_full[j % KS], (j / KS) & 1)) return false;
       if (j > 0 && !mbar_wait_warp(s_read, (j - 1) & 1)) return false;
       tc_fence_after();
-      mma_tmem_abt(tmem, tmem + 384, kd + (uint64_t)(j % KS) * ST);
+      mma_abt(tmem, qd, kd + (uint64_t)(j % KS) * ST);
       umma_commit(s_full);
       return true;
     };
     auto issue_dp = [&](int j) {
       if (!mbar_wait_warp(&v_full[j % VS], (j / VS) & 1)) return false;
       tc_fence_after();
-      mma_tmem_abt(tmem + 128, tmem + 448, vd + (uint64_t)(j % VS) * ST);
+      mma_abt(tmem + 128, dd, vd + (uint64_t)(j % VS) * ST);
       umma_commit(dp_full);
       umma_commit(&v_empty[j % VS]);
       return true;
     };
-    bool ok = mbar_wait_warp(q_ready, 0) && issue_s(0) && issue_dp(0) && (n_k < 2 || issue_s(1));
+    bool ok = mbar_wait_warp(qd_full, 0) && issue_s(0) && issue_dp(0) && (n_k < 2 || issue_s(1));
     for (int j = 0; j < n_k && ok; ++j) {
+      if (!mbar_wait_warp(p_ready, j & 1)) { ok = false; break; }
+      tc_fence_after();
+      mma_tmem_ab(tmem + 384, tmem + 128, kd_mn + (uint64_t)(j % KS) * ST, j != 0);
       if (!mbar_wait_warp(ds_ready, j & 1)) { ok = false; break; }
       tc_fence_after();
-      mma_tmem_ab(tmem + 256, tmem + 128, kd_mn + (uint64_t)(j % KS) * ST, j != 0);
+      mma_tmem_ab(tmem + 256, tmem + 128 + 16, kd_mn + (uint64_t)(j % KS) * ST, j != 0);
       umma_commit(&k_empty[j % KS]);
       ok = (j + 1 >= n_k || issue_dp(j + 1)) && (j + 2 >= n_k || issue_s(j + 2));
     }
@@ -542,30 +524,43 @@ __device__ __forceinline__ void query_tile(const BwdMaps& maps, const BwdArgs& p
     const int r = qw * 32 + lane;  // query row of the tile
     const uint32_t lanes = (uint32_t)(qw * 32) << 16;
     const uint32_t tS = tmem + lanes + g * 32, tP = tS + 128;
-    {  // this warp's 32 of the row's 128 columns of Q and dO into TMEM
-      uint4 a[4], b[4];
-      const uint4* qs = reinterpret_cast<const uint4*>(q + ((long)h * L_pad + row0 + r) * 128) + g * 4;
-      const uint4* ds = reinterpret_cast<const uint4*>(d + (long)(row0 + r) * H * 128 + h * 128) + g * 4;
+    const long at = (long)h * L_pad + row0 + r;
+    const bool in = row0 + r < L;
+    float* sums = reinterpret_cast<float*>(smem + Y::SUM) + r;
+    // a sum over the row's four warps, added in the same order by each
+    auto row_sum = [&](float part) {
+      sums[g * 128] = part;
+      named_barrier_sync(1, CWARPS * 32);
+      return (sums[0] + sums[128]) + (sums[256] + sums[384]);
+    };
+    const float nl = in ? -p.lse[at] * 1.4426950408889634f : -INFINITY;
+    float nd = 0.f;
+    if (in) {
+      const long col = (long)(row0 + r) * H * 128 + h * 128 + g * 32;
+      const uint4 *po = reinterpret_cast<const uint4*>(p.o + col), *pd = reinterpret_cast<const uint4*>(p.d + col);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        a[i] = row0 + r < L ? __ldg(qs + i) : make_uint4(0, 0, 0, 0);
-        b[i] = row0 + r < L ? __ldg(ds + i) : make_uint4(0, 0, 0, 0);
+        const uint4 u = __ldg(po + i), w = __ldg(pd + i);
+        const __nv_bfloat162 *pu = reinterpret_cast<const __nv_bfloat162*>(&u),
+                             *pw = reinterpret_cast<const __nv_bfloat162*>(&w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 x = __bfloat1622float2(pu[e]), y = __bfloat1622float2(pw[e]);
+          nd = fmaf(-x.x, y.x, nd);
+          nd = fmaf(-x.y, y.y, nd);
+        }
       }
-      tmem_st16(tmem + lanes + 384 + g * 16, reinterpret_cast<const uint32_t*>(a));
-      tmem_st16(tmem + lanes + 448 + g * 16, reinterpret_cast<const uint32_t*>(b));
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_ready);
     }
-    const float nl = p.nlse2[(long)h * L_pad + row0 + r], nd = p.ndelta[(long)h * L_pad + row0 + r];
+    nd = row_sum(nd);
     const uint64_t sc2 = f2_pack(scale_log2, scale_log2), nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
+    uint64_t ds_sum = 0ull;  // of this warp's columns of the row, as they are before their rounding
     bool ok = true;
     for (int j = 0; j < n_k; ++j) {
       ok = mbar_wait_warp(s_full, j & 1);
       if (!ok) break;
       tc_fence_after();
       float pr[32], dp[32];
+      uint32_t pk[16];
       tmem_ld32(tS, reinterpret_cast<uint32_t*>(pr));
       tmem_wait_ld();
       tc_fence_before();
@@ -579,31 +574,56 @@ __device__ __forceinline__ void query_tile(const BwdMaps& maps, const BwdArgs& p
         for (int c = 0; c < 32; ++c)
           if (c >= valid) pr[c] = 0.f;
       }
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) pk[c / 2] = pack_bf16x2(pr[c], pr[c + 1]);
       ok = mbar_wait_warp(dp_full, j & 1);
       if (!ok) break;
       tc_fence_after();
       tmem_ld32(tP, reinterpret_cast<uint32_t*>(dp));
       tmem_wait_ld();
-      uint32_t pk[16];
+      // the warp's own 32 columns of dP are read: P over the first 16
+      tmem_st16(tP, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_ready);
 #pragma unroll
       for (int c = 0; c < 32; c += 2) {
+        const uint64_t ds = f2_mul(f2_pack(pr[c], pr[c + 1]), f2_add(f2_pack(dp[c], dp[c + 1]), nd2));
+        ds_sum = f2_add(ds_sum, ds);
         float a, b;
-        f2_unpack(f2_mul(f2_pack(pr[c], pr[c + 1]), f2_add(f2_pack(dp[c], dp[c + 1]), nd2)), a, b);
+        f2_unpack(ds, a, b);
         pk[c / 2] = pack_bf16x2(a, b);
       }
-      // the warp's own 32 columns of dP are read: dS over the first 16
-      tmem_st16(tP, pk);
+      tmem_st16(tP + 16, pk);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(ds_ready);
     }
+    // (every warp has left the sums above before the first tile's dS K)
+    float s0, s1;
+    f2_unpack(ds_sum, s0, s1);
+    const float rest = row_sum(s0 + s1);
     ok = ok && mbar_wait_warp(acc_full, 0);
     if (ok) {
       tc_fence_after();
-      bf16* dst = dq + ((long)h * L_pad + row0 + r) * 128 + g * 32;
-      store_cols32(tmem + lanes + 256 + g * 32, scale, dst);
-      if (row0 + r >= L) zero_cols32(dst);
+      bf16* dst = dq + at * 128 + g * 32;
+      float a[32], b[32];
+      tmem_ld32(tmem + lanes + 256 + g * 32, reinterpret_cast<uint32_t*>(a));
+      tmem_ld32(tmem + lanes + 384 + g * 32, reinterpret_cast<uint32_t*>(b));
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 32; ++c) a[c] = fmaf(-rest, b[c], a[c]) * scale;
+#pragma unroll
+      for (int c = 0; c < 32; c += 8)
+        *reinterpret_cast<uint4*>(dst + c) = make_uint4(pack_bf16x2(a[c], a[c + 1]), pack_bf16x2(a[c + 2], a[c + 3]),
+                                                        pack_bf16x2(a[c + 4], a[c + 5]), pack_bf16x2(a[c + 6], a[c + 7]));
+      if (!in) zero_cols32(dst);
+      if (g == 0) {
+        p.nlse2[at] = nl;
+        p.ndelta[at] = in ? nd - rest : 0.f;
+      }
     }
   }
   tc_fence_before();
@@ -614,8 +634,9 @@ __device__ __forceinline__ void query_tile(const BwdMaps& maps, const BwdArgs& p
   }
 }
 
-// CTAs [0, n H) take the key tiles, which are the longer work, the others the
-// query tiles: one launch, and one tail instead of two.
+// A CTA a tile: KEYS the key tiles, else the query tiles, which go first and
+// leave the deltas that the key tiles read.
+template <bool KEYS>
 __global__ void __launch_bounds__(THREADS, 1)
     attention_bwd_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs p, int n) {
   // seven tiles leave no room to align the base by hand: the swizzled tiles
@@ -626,13 +647,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (threadIdx.x == 0) atomicCAS(&g_h3_device_error, 0, 1);
     return;
   }
-  int b = blockIdx.x;
-  if (b < n * p.H) {
-    key_tile(maps, p, b % n, b / n, smem_bwd);
-  } else {
-    b -= n * p.H;
-    query_tile(maps, p, b % n, b / n, smem_bwd);
-  }
+  if constexpr (KEYS)
+    key_tile(maps, p, blockIdx.x % n, blockIdx.x / n, smem_bwd);
+  else
+    query_tile(maps, p, blockIdx.x % n, blockIdx.x / n, smem_bwd);
 }
 
 // [H][L_pad][128] heads as 64 x 128-row boxes whose rows end at L
@@ -655,23 +673,20 @@ cudaError_t launch_attention_bwd(const bf16* q, const bf16* k, const bf16* v, co
                                  const bf16* d, int H, int L, int L_pad, float scale, float scale_log2, bf16* dq,
                                  bf16* dk, bf16* dv, float* ws, cudaStream_t stream) {
   using namespace attn_bwd;
-  static unsigned long long done = 0;
-  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(attention_bwd_kernel), KvLayout::BYTES, &done);
+  static unsigned long long done[2] = {0, 0};
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(attention_bwd_kernel<false>), QLayout::BYTES, &done[0]);
+  if (e != cudaSuccess) return e;
+  e = ensure_smem_attr(reinterpret_cast<const void*>(attention_bwd_kernel<true>), KvLayout::BYTES, &done[1]);
   if (e != cudaSuccess) return e;
   BwdMaps maps;
   if (!make_tmap_heads(&maps.q, q, H, L, L_pad) || !make_tmap_heads(&maps.k, k, H, L, L_pad) ||
       !make_tmap_heads(&maps.v, v, H, L, L_pad) || !make_tmap_bf16(&maps.d, d, L, 128L * H, 128L * H, 128))
     return cudaErrorInvalidValue;
-  float* nlse2 = ws;
-  float* ndelta = ws + (size_t)H * L_pad;
-  const long pieces = (long)L_pad * H * 16;
-  const long blocks = (pieces + 255) / 256, most = (long)num_sms() * 16;
-  e = launch_chained(attention_delta_kernel, dim3((int)(blocks < most ? blocks : most)), 256, 0, stream, o, d, lse, H, L,
-                     L_pad, nlse2, ndelta);
-  if (e != cudaSuccess) return e;
   const int n = L_pad / attn_detail::TILE;
-  const BwdArgs args{q, d, nlse2, ndelta, H, L, L_pad, scale, scale_log2, dq, dk, dv};
-  return launch_chained(attention_bwd_kernel, dim3(2 * n * H), THREADS, KvLayout::BYTES, stream, maps, args, n);
+  const BwdArgs args{o, d, lse, ws, ws + (size_t)H * L_pad, H, L, L_pad, scale, scale_log2, dq, dk, dv};
+  e = launch_chained(attention_bwd_kernel<false>, dim3(n * H), THREADS, QLayout::BYTES, stream, maps, args, n);
+  if (e != cudaSuccess) return e;
+  return launch_chained(attention_bwd_kernel<true>, dim3(n * H), THREADS, KvLayout::BYTES, stream, maps, args, n);
 }
 
 }  // namespace h3
