@@ -556,7 +556,7 @@ enum h3_backward_op {
 };
 
 /* Host only.  Workspace bytes of one backward call at L_pad rows (0 for
- * invalid arguments). */
+ * dims, rows or an operation that the call itself would refuse). */
 size_t h3_backward_workspace_bytes(const h3_dims* dims, int L_pad, int op);
 
 /* Backward of h3_adaln_norm_modulate (same x, mod, branch), joined with the

@@ -72,7 +72,7 @@ const bf16* b16(const h3_bf16* p) { return reinterpret_cast<const bf16*>(p); }
 extern "C" {
 
 size_t h3_backward_workspace_bytes(const h3_dims* dims, int L_pad, int op) {
-  if (!dims || L_pad <= 0 || dims->D <= 0 || dims->H <= 0 || dims->I <= 0 || dims->F <= 0) return 0;
+  if (check_dims(dims, __func__) != H3_OK || L_pad <= 0 || L_pad % 128 != 0) return 0;
   Carve c(nullptr);
   switch (op) {
     case H3_BWD_ADALN: c.take<float>((size_t)adaln_bwd_parts(dims->D) * 2 * dims->D); break;
