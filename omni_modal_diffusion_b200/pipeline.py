@@ -299,9 +299,26 @@ class H3BlockTrain:
                               h3.H3_BWD_FFN))
         self.ws = e(max(need, 2 * Lp * F), dt=torch.uint8)
 
+    def _check(self, name, x, mod, pos, W):
+        """Sizes and devices of a call's tensors, before anything reads them: the library's
+        forward calls see only pointers."""
+        d, Lp = self.dims, self.ranges.L_pad
+        missing = [n for n in self.WEIGHTS if n not in W]
+        if missing:
+            raise ValueError(f"weights missing: {', '.join(missing)}")
+        counts = {"Wqkv": 3 * d.I * d.D, "qn_w": 128, "kn_w": 128, "Wo": d.D * d.I, "Wgu": 2 * d.F * d.D, "Wd": d.D * d.F}
+        for n, t, count in ((name, x, Lp * d.D), ("mod", mod, 18 * d.D), ("pos", pos, Lp * 3),
+                            *((n, W[n], c) for n, c in counts.items())):
+            if t.numel() != count:
+                raise ValueError(f"{n} must have {count} elements, got {t.numel()}")
+            if t.device != self.x0.device:
+                raise ValueError(f"{n} is on {t.device}, the block on {self.x0.device}")
+
     def forward(self, x, mod, pos, W, stream=None):
         """x fp32 [L_pad][D], updated in place (the same values as
-        h3_block_forward's); mod [3][6][D]; W: the block's weights by name."""
+        h3_block_forward's); mod [3][6][D]; pos [L_pad][3]; W: the block's
+        weights by name."""
+        self._check("x", x, mod, pos, W)
         d, r = self.dims, self.ranges
         with torch.cuda.stream(stream or torch.cuda.current_stream(self.device)):
             self.x0.copy_(x)
@@ -317,6 +334,7 @@ class H3BlockTrain:
         """dx fp32 [L_pad][D]: the gradient of the block's output, replaced by
         that of its input.  Returns bf16 gradients by weight name and "mod"
         ([3][6][D]); names in `frozen` are not computed."""
+        self._check("dx", dx, mod, pos, W)
         d, r = self.dims, self.ranges
         unknown = set(frozen) - set(self.WEIGHTS) - {"mod"}
         if unknown:
