@@ -298,10 +298,11 @@ class H3BlockTrain:
                    for op in (h3.H3_BWD_ADALN, h3.H3_BWD_QKV, h3.H3_BWD_ATTENTION, h3.H3_BWD_GATED_RESIDUAL,
                               h3.H3_BWD_FFN))
         self.ws = e(max(need, 2 * Lp * F), dt=torch.uint8)
+        self.kept = False  # whether a forward call has run
 
     def _check(self, name, x, mod, pos, W):
-        """Sizes and devices of a call's tensors, before anything reads them: the library's
-        forward calls see only pointers."""
+        """Sizes and devices of a call's tensors, before anything reads them:
+        the library's forward calls see only pointers."""
         d, Lp = self.dims, self.ranges.L_pad
         missing = [n for n in self.WEIGHTS if n not in W]
         if missing:
@@ -329,6 +330,7 @@ class H3BlockTrain:
             self.x1.copy_(x)
             h3.h3_adaln_norm_modulate(d, r, x, mod, h3.H3_MLP, self.xm)
             h3.h3_ffn_swiglu(d, r, x, self.xm, W["Wgu"], W["Wd"], mod, self.ws[:2 * r.L_pad * d.F].view(torch.bfloat16))
+        self.kept = True
 
     def backward(self, dx, mod, pos, W, frozen=(), stream=None) -> dict:
         """dx fp32 [L_pad][D]: the gradient of the block's output, replaced by
@@ -339,6 +341,8 @@ class H3BlockTrain:
         unknown = set(frozen) - set(self.WEIGHTS) - {"mod"}
         if unknown:
             raise ValueError(f"unknown names in frozen: {sorted(unknown)}")
+        if not self.kept:
+            raise RuntimeError("backward() reads what forward() keeps: call forward() first")
         with torch.cuda.stream(stream or torch.cuda.current_stream(self.device)):
             g = {n: torch.empty_like(W[n]) for n in self.WEIGHTS if n not in frozen}
             if "mod" not in frozen:

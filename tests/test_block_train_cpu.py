@@ -55,3 +55,10 @@ def test_tensors_on_another_device(block, call, name):
     where[name] = where[name].to("meta")
     with pytest.raises(ValueError, match=f"{'dx' if (name, call) == ('x', 'backward') else name} is on meta"):
         getattr(block, call)(a["x"], a["mod"], a["pos"], a["W"])
+
+
+def test_backward_comes_after_forward(block):
+    """Until a forward call has run, what backward reads of it is not there."""
+    a = arguments()
+    with pytest.raises(RuntimeError, match="forward"):
+        block.backward(a["x"], a["mod"], a["pos"], a["W"])
