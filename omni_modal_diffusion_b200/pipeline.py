@@ -338,7 +338,8 @@ class H3BlockTrain:
         ([3][6][D]); names in `frozen` are not computed."""
         self._check("dx", dx, mod, pos, W)
         d, r = self.dims, self.ranges
-        unknown = set(frozen) - set(self.WEIGHTS) - {"mod"}
+        frozen = set(frozen)
+        unknown = frozen - set(self.WEIGHTS) - {"mod"}
         if unknown:
             raise ValueError(f"unknown names in frozen: {sorted(unknown)}")
         if not self.kept:
