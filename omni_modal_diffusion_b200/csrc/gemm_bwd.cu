@@ -696,8 +696,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
           const float gate = in ? __ldg(p.mod + (long)(sg * 6 + p.gate_slot) * pr.M + m) : 0.f;
           if (!wait_full()) break;
           const uint32_t tb = tmem_base + lane_off + (uint32_t)(acc * 256 + sub * COLS);
-          // eight columns at a time: with 16 more of the sums spill (out-projection
-          // at 512 tokens 87.6 us, so 85.7; at 2,048 tokens 262 and 258)
+          // eight columns at a time, with a few words of spills (36 bytes stored, 28
+          // loaded); with 16 more of the sums spill (out-projection at 512 tokens
+          // 87.6 us, so 85.7; at 2,048 tokens 262 and 258)
           float dot = 0.f;
 #pragma unroll
           for (int c = 0; c < COLS; c += 8) {
